@@ -54,7 +54,16 @@ typedef enum {
 /* Storage formats.  MOE_Q4_K and MOE_Q4_K_Q6_K are expert-weight formats only
  * (the k-quant stacks of the Metal MoE providers, ferrum-kernels vnext MoE:
  * "q4k" for all projections, "q4k_q6k" for Q4_K gate/up with Q6_K down). */
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_Q8_0 = 2, MOE_Q4_K = 3, MOE_Q4_K_Q6_K = 4 } moe_dtype;
+typedef enum {
+  MOE_F32 = 0,
+  MOE_BF16 = 1,
+  MOE_Q8_0 = 2,
+  MOE_Q4_K = 3,
+  MOE_Q4_K_Q6_K = 4,
+  MOE_FP8 = 8,   /* expert weights: e4m3 codes with one f32 scale per 128 x 128 block (see moe_weights) */
+  MOE_E4M3 = 16, /* 8-bit float codes of moe_fp8_quantize and moe_fp8_gemm: 4 exponent bits, largest value 448 */
+  MOE_E5M2 = 17  /* 5 exponent bits, largest value 57344 */
+} moe_dtype;
 
 /* SiLU(g) = g / (1 + e^-g)  (hf2q qwen35/gpu_ffn.rs, silu_mul_cpu);
  * GELU_TANH(g) = 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))
@@ -71,7 +80,7 @@ typedef struct moe_desc {
   int32_t act;             /* moe_act, used by routed and shared experts */
   int32_t renormalize;     /* 1: selected gate values divided by their sum; 0: the gate values themselves */
   int32_t act_dtype;       /* MOE_F32 | MOE_BF16: x and out */
-  int32_t w_dtype;         /* MOE_F32 | MOE_BF16 | MOE_Q8_0 | MOE_Q4_K | MOE_Q4_K_Q6_K: expert and shared
+  int32_t w_dtype;         /* MOE_F32 | MOE_BF16 | MOE_Q8_0 | MOE_Q4_K | MOE_Q4_K_Q6_K | MOE_FP8: expert and shared
                               projections (the k-quant formats need H, I and shared_I multiples of 256) */
   int32_t router_dtype;    /* MOE_F32 | MOE_BF16: router W and the shared-gate vector w_s */
   int32_t has_router_bias; /* 1: logits += b_e before selection (ferrox-models decoder.rs, gpt_oss_ffn) */
@@ -102,6 +111,15 @@ typedef struct moe_desc {
  * [E*H, I/256, 192] bytes (ql then qh of each block) and down_scale
  * [E*H, srow] bytes with srow = ceil(18 * I/256 / 16) * 16: the 16 scales of
  * every block of the row, then the fp16 d of every block, then zeros.
+ * For MOE_FP8 the projection pointers hold e4m3 codes with the f32 shapes and the
+ * *_scale pointers one f32 scale per 128 x 128 block of each matrix (the last
+ * block of a row or column may be partial): gate_scale and up_scale
+ * [E, ceil(I/128), ceil(H/128)], down_scale [E, ceil(H/128), ceil(I/128)],
+ * sh_gate_scale and sh_up_scale [ceil(Is/128), ceil(H/128)], sh_down_scale
+ * [ceil(H/128), ceil(Is/128)]; value = scale * code.  moe_fp8_quantize_weights()
+ * makes this form.  Every product of such a layer takes 8-bit operands: x is
+ * coded as by moe_fp8_quantize (e4m3, one scale per 128 values of a token), so
+ * is h = act(gate) * up (per 128 values of a pair's row), and sums are f32.
  * All weight pointers are 16-byte aligned.  Unused pointers may be NULL.
  */
 typedef struct moe_weights {
@@ -214,7 +232,8 @@ moe_status moe_combine(const moe_desc* d, const float* y_slots, const void* x, c
  * The whole layer in one call: route, permute, experts, shared expert, combine.
  * Picks the tensor-core path (tcgen05 grouped GEMMs) when x and the expert
  * weights are bf16 and T > 64, else the weight-streaming path.  The
- * streaming path stages whole token rows in shared memory and returns
+ * streaming path (MOE_FP8 weights have their own tensor-core kernels for every T)
+ * stages whole token rows in shared memory and returns
  * MOE_ERR_UNSUPPORTED (also from moe_expert_ffn / moe_combine) when
  * H * sizeof(act) > 65536 or I * 4 > 65536 or shared_I * 4 > 65536.
  * On the tensor-core path each expert's output row is kept in bf16 and the
@@ -321,6 +340,120 @@ moe_status moe_act_up_backward(int64_t P, int64_t I, int32_t act, const float* g
  */
 moe_status moe_q6_k_split(const void* blocks, int64_t rows, int64_t cols, void* q, void* scales,
                           moe_stream_t stream);
+
+/*
+ * Expert selection from router logits with a balance bias that moves the
+ * choice and not the weights, and its gradient: the routing a training user
+ * runs on moe_route's logits or its own, in front of moe_experts.
+ *
+ * Per token, with logits l [E]:
+ *   scores  s_e = softmax(l)_e or 1/(1+e^-l_e) (scoring, a moe_gating); an
+ *           expert whose logit is -inf is masked: it scores 0 and is chosen
+ *           only when fewer than top_k others are eligible
+ *   keys    without a bias the logits (the scores' order); with one s_e + b_e,
+ *           compared in 64 bits
+ *   groups  n_groups > 1: the experts form n_groups contiguous groups; a group
+ *           scores its largest key (MOE_GROUP_MAX) or the sum of its two largest
+ *           s_e + b_e in 64 bits (MOE_GROUP_TOP2; of its one in groups of one);
+ *           only the topk_groups best (lower index on ties) are eligible
+ *   ids     the top_k largest keys in order, the lower expert first on ties
+ *   w_k     scale * s_{ids_k}, divided by sum_j s_{ids_j} when renormalize (a
+ *           sum of 0 gives weights 0)
+ * NaN logits or keys sort like -inf; the ids are distinct and in range whatever
+ * the logits hold.  Limits as above (E <= 256, top_k <= 32, n_groups <= 32).
+ *
+ *  logits  [T, E] of logits_dtype (MOE_F32 | MOE_BF16), rows `stride` elements apart (stride >= E), no
+ *          alignment beyond the type's
+ *  bias    [E] f32 or NULL
+ *  ids     [T, top_k] int32 out; w [T, top_k] f32 out; scores [T, E] f32 out or NULL
+ *  T == 0 does nothing.
+ */
+typedef enum { MOE_GROUP_MAX = 0, MOE_GROUP_TOP2 = 1 } moe_group_score;
+typedef struct moe_select_desc {
+  int32_t T, E, top_k;
+  int32_t scoring;       /* moe_gating */
+  int32_t n_groups;      /* 0 or 1: no groups */
+  int32_t topk_groups;
+  int32_t group_score;   /* moe_group_score */
+  int32_t renormalize;   /* 0 | 1 */
+  int32_t logits_dtype;  /* MOE_F32 | MOE_BF16 */
+  float scale;
+} moe_select_desc;
+moe_status moe_select(const moe_select_desc* d, const void* logits, int64_t stride, const float* bias, int32_t* ids,
+                      float* w, float* scores, moe_stream_t stream);
+
+/*
+ * Gradient of moe_select's weights (and scores) with the selection held
+ * constant.  With n_k = s_k / S, S = sum_k s_k over the chosen experts,
+ *   ds_k = scale / S (d_w_k - sum_j d_w_j n_j)   (renormalize; 0 when S is 0)
+ *   ds_k = scale d_w_k                           (otherwise)
+ * plus d_scores_e where given (the gradient of a balance loss on the scores);
+ *   softmax: d_logits_e = s_e (ds_e - sum_j ds_j s_j);  sigmoid: ds_e s_e (1 - s_e).
+ *  d describes the forward call (groups and bias do not enter); ids [T, top_k]
+ *  as chosen (ids outside [0, E) count nothing and are reported as
+ *  MOE_ERR_DEVICE_INDEX; an expert named twice counts twice); d_w [T, top_k] f32;
+ *  d_scores [T, E] f32 or NULL; d_logits [T, E] out, dense, of logits_dtype.
+ *  The same bits on every run.
+ */
+moe_status moe_select_backward(const moe_select_desc* d, const void* logits, int64_t stride, const int32_t* ids,
+                               const float* d_w, const float* d_scores, void* d_logits, moe_stream_t stream);
+
+/*
+ * Block-scaled 8-bit floats.  A block of values shares one f32 scale; with
+ * a = max(max|x|, 2^-100) over the block and top = 448 (MOE_E4M3) or 57344
+ * (MOE_E5M2):
+ *   scale = a / top, inv = top / a, both rounded to f32   (pow2_scales == 0)
+ *   scale = 2^ceil(log2(a / top)), inv = 1 / scale        (pow2_scales == 1)
+ *   code  = the format's nearest value, half to even, of the f32 product x * inv
+ * and value = scale * code.  A NaN or infinity makes its block's values NaN.
+ *
+ * moe_fp8_quantize: rows x [R, C] (MOE_F32 | MOE_BF16, `stride` elements apart), one scale per 128 consecutive
+ * values of a row (the last block may be partial): q [R, C] codes, scales [ceil(C/128), R] f32 -- block-major,
+ * so that the scales of one block of consecutive rows are consecutive.
+ * moe_fp8_quantize_weights: w [G, N, K] dense, one scale per 128 x 128 block of each matrix: q [G, N, K] codes,
+ * scales [G, ceil(N/128), ceil(K/128)] f32.
+ * C, K multiples of 32; N any; x, w and q 16-byte aligned, x's rows too; R, N <= 2^25, C, K <= 2^20,
+ * G <= 65535, N <= 2^22 for the weights.  R * C == 0 (G * N * K == 0) does nothing.
+ */
+moe_status moe_fp8_quantize(const void* x, int32_t x_dtype, int64_t R, int64_t C, int64_t stride, int32_t format,
+                            int32_t pow2_scales, void* q, float* scales, moe_stream_t stream);
+moe_status moe_fp8_quantize_weights(const void* w, int32_t w_dtype, int64_t G, int64_t N, int64_t K, int32_t format,
+                                    int32_t pow2_scales, void* q, float* scales, moe_stream_t stream);
+
+/*
+ * Product of block-scaled 8-bit floats, dense or grouped (out x in, as every
+ * weight of this library):
+ *   out[r, n] = sum_kb a_scales[kb, r] b_scales[g, n/128, kb] sum_{k in block kb} a[r, k] b[g, n, k]
+ * for the rows offsets[g] <= r < offsets[g+1] of group g; f32 sums, one scale
+ * multiplication per block of 128.  Rows in no group are left as they were.
+ *  a [M, K], a_scales [ceil(K/128), M]: moe_fp8_quantize's form (a_format)
+ *  b [G, N, K], b_scales [G, ceil(N/128), ceil(K/128)]: moe_fp8_quantize_weights' form (b_format)
+ *  offsets [G+1] int32 device, ascending, or NULL for G == 1 (all rows); values outside [0, M] are clamped and
+ *          reported as MOE_ERR_DEVICE_INDEX
+ *  out [M, N] of out_dtype (MOE_F32 | MOE_BF16)
+ * The gradient with respect to the rows is the same product with the stack
+ * transposed ([G, K, N], its block scales transposed).
+ * N, K multiples of 32, N, K <= 2^20; M <= 2^25; G <= 256.  M == 0 does nothing.
+ */
+moe_status moe_fp8_gemm(int64_t M, int64_t N, int64_t K, int64_t G, const void* a, const float* a_scales,
+                        int32_t a_format, const void* b, const float* b_scales, int32_t b_format,
+                        const int32_t* offsets, void* out, int32_t out_dtype, moe_stream_t stream);
+
+/*
+ * The layer on a routing of the caller's (moe_select's, or any other): permute,
+ * experts, shared expert, combine:
+ *   out[t] = sum_k topk_w[t,k] expert_{topk_ids[t,k]}(x_t) + s_t shared(x_t)
+ * moe_layer without its router; every w_dtype.  A pair whose id is outside
+ * [0, E) counts nothing and is reported as MOE_ERR_DEVICE_INDEX.  An expert may
+ * appear twice in a token's ids.
+ *  topk_ids [T,K] int32, topk_w [T,K] f32; shared_gate [T] f32 (required iff shared_I > 0 and has_shared_gate,
+ *  else ignored); x, out, w, ws as for moe_layer (w->router and the routing fields of d are not used).
+ * The MOE_FP8 slot rows are kept in act_dtype (bf16 slots as in moe_layer's
+ * tensor-core path) and added in slot order in f32.
+ */
+moe_status moe_experts(const moe_desc* d, const void* x, const moe_weights* w, const int32_t* topk_ids,
+                       const float* topk_w, const float* shared_gate, void* out, void* ws, size_t ws_bytes,
+                       moe_stream_t stream);
 
 /*
  * Synchronises `stream`, then returns and clears the device status word of

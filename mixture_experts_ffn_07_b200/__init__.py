@@ -17,12 +17,14 @@ from dataclasses import dataclass, fields
 
 from . import _lib
 from ._lib import (MOE_ACT_GELU_TANH, MOE_ACT_SILU, MOE_BF16, MOE_ERR_CUDA, MOE_ERR_DEVICE_INDEX,  # noqa: F401
-                   MOE_ERR_INVALID_ARG, MOE_ERR_TIMEOUT, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_F32, MOE_OK,
+                   MOE_E4M3, MOE_E5M2, MOE_ERR_INVALID_ARG, MOE_ERR_TIMEOUT, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_F32, MOE_FP8, MOE_OK,
                    MOE_Q4_K, MOE_Q4_K_Q6_K, MOE_Q8_0, MoeError, check, status_string)
 
-DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "q8_0": MOE_Q8_0, "q4_k": MOE_Q4_K, "q4_k_q6_k": MOE_Q4_K_Q6_K}
+DTYPES = {"f32": MOE_F32, "bf16": MOE_BF16, "q8_0": MOE_Q8_0, "q4_k": MOE_Q4_K, "q4_k_q6_k": MOE_Q4_K_Q6_K,
+          "fp8": MOE_FP8}
 ACTS = {"silu": MOE_ACT_SILU, "gelu_tanh": MOE_ACT_GELU_TANH}
 GATINGS = {"softmax": 0, "sigmoid": 1}  # moe_gating
+GROUP_SCORES = {"max": 0, "top2": 1}  # moe_group_score
 
 
 @dataclass
@@ -56,8 +58,27 @@ class Desc:
 
 
 @dataclass
+class SelectDesc:
+    """moe_select_desc: how `select` chooses and weights the experts of T tokens from logits [T, E]."""
+    T: int
+    E: int
+    top_k: int
+    scoring: str = "softmax"
+    n_groups: int = 1
+    topk_groups: int = 1
+    group_score: str = "max"
+    renormalize: bool = True
+    scale: float = 1.0
+
+    def c(self, logits_dtype: int) -> _lib.MoeSelectDesc:
+        return _lib.MoeSelectDesc(self.T, self.E, self.top_k, GATINGS[self.scoring], self.n_groups, self.topk_groups,
+                                  GROUP_SCORES[self.group_score], int(self.renormalize), logits_dtype, self.scale)
+
+
+@dataclass
 class Weights:
-    """Device tensors, out x in.  For Q8_0 the projections are int8 and *_scale hold fp16 block scales."""
+    """Device tensors, out x in.  For Q8_0 the projections are int8 and *_scale hold fp16 block scales; for fp8
+    they are float8_e4m3fn and *_scale hold one f32 scale per 128 x 128 block."""
     router: object = None
     router_bias: object = None
     gate: object = None
@@ -181,6 +202,157 @@ def q6_k_split(blocks, rows, cols, q, scales, stream=None):
 def q6_k_srow_bytes(cols: int) -> int:
     """Bytes of one scale row of the Q6_K split form (include/moe.h)."""
     return (cols // 256 * 18 + 15) // 16 * 16
+
+
+class _Types:
+    """moe_dtype of each torch dtype that an argument of the calls below may have (made at the first call, so that
+    importing the package does not import torch)."""
+    i32 = f32 = act = fp8 = None
+
+    @classmethod
+    def ready(cls):
+        if cls.i32 is None:
+            import torch
+            cls.i32 = {torch.int32: 0}
+            cls.f32 = {torch.float32: MOE_F32}
+            cls.act = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+            cls.bf16 = {torch.bfloat16: MOE_BF16}
+            cls.fp8 = {torch.float8_e4m3fn: MOE_E4M3, torch.float8_e5m2: MOE_E5M2}
+        return cls
+
+
+def _arg(name, t, types, shape, device=None, dense=True):
+    """Checks a tensor argument and returns the code of its type.  `device`: the index it has to be on."""
+    code = types.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name}: {t.dtype}, expected one of {list(types)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    dev = t.get_device()
+    if dev < 0 or (device is not None and dev != device):
+        raise ValueError(f"{name} is on {t.device}" + ("" if device is None else f", not on cuda:{device}"))
+    return code
+
+
+def _row_stride(name, t):
+    """Elements between the rows of a 2-D tensor whose rows are dense."""
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row are not consecutive")
+    return t.stride(0) if rows > 1 else max(cols, 1)
+
+
+def _call(device, fn, name, *args, stream):
+    """One library call with `device` current, on `stream` (default: that device's current stream)."""
+    import torch
+    prev = torch.cuda.current_device()
+    if prev == device:
+        check(fn(*args, _stream(stream)), name)
+        return
+    with torch.cuda.device(device):
+        check(fn(*args, _stream(stream)), name)
+
+
+def select(desc, logits, ids, w, bias=None, scores=None, stream=None):
+    """moe_select: logits [T,E] (f32 or bf16, rows may be padded) -> ids [T,K] int32, w [T,K] f32
+    (, scores [T,E] f32).  bias [E] f32 moves the choice, not the weights."""
+    ty = _Types.ready()
+    T, E, K = desc.T, desc.E, desc.top_k
+    code = _arg("logits", logits, ty.act, (T, E), dense=False)
+    ld, dev = _row_stride("logits", logits), logits.get_device()
+    _arg("ids", ids, ty.i32, (T, K), dev)
+    _arg("w", w, ty.f32, (T, K), dev)
+    if bias is not None:
+        _arg("bias", bias, ty.f32, (E,), dev)
+    if scores is not None:
+        _arg("scores", scores, ty.f32, (T, E), dev)
+    _call(dev, _lib.lib().moe_select, "moe_select", ctypes.byref(desc.c(code)), logits.data_ptr(), ld, _ptr(bias),
+          ids.data_ptr(), w.data_ptr(), _ptr(scores), stream=stream)
+
+
+def select_backward(desc, logits, ids, d_w, d_logits, d_scores=None, stream=None):
+    """moe_select_backward: d_w [T,K] f32 (, d_scores [T,E] f32) -> d_logits [T,E] of the logits' type."""
+    ty = _Types.ready()
+    T, E, K = desc.T, desc.E, desc.top_k
+    code = _arg("logits", logits, ty.act, (T, E), dense=False)
+    ld, dev = _row_stride("logits", logits), logits.get_device()
+    _arg("ids", ids, ty.i32, (T, K), dev)
+    _arg("d_w", d_w, ty.f32, (T, K), dev)
+    if d_scores is not None:
+        _arg("d_scores", d_scores, ty.f32, (T, E), dev)
+    if _arg("d_logits", d_logits, ty.act, (T, E), dev) != code:
+        raise ValueError(f"d_logits: {d_logits.dtype}, expected {logits.dtype}")
+    _call(dev, _lib.lib().moe_select_backward, "moe_select_backward", ctypes.byref(desc.c(code)), logits.data_ptr(),
+          ld, ids.data_ptr(), d_w.data_ptr(), _ptr(d_scores), d_logits.data_ptr(), stream=stream)
+
+
+def fp8_quantize(x, q, scales, pow2=False, stream=None):
+    """moe_fp8_quantize: x [R,C] (f32 or bf16, rows may be padded) -> q [R,C] (float8_e4m3fn or float8_e5m2),
+    scales [ceil(C/128), R] f32."""
+    ty = _Types.ready()
+    R, C = x.shape
+    code = _arg("x", x, ty.act, (R, C), dense=False)
+    ld, dev = _row_stride("x", x), x.get_device()
+    fmt = _arg("q", q, ty.fp8, (R, C), dev)
+    _arg("scales", scales, ty.f32, ((C + 127) // 128, R), dev)
+    _call(dev, _lib.lib().moe_fp8_quantize, "moe_fp8_quantize", x.data_ptr(), code, R, C, ld, fmt, int(pow2),
+          q.data_ptr(), scales.data_ptr(), stream=stream)
+
+
+def fp8_quantize_weights(w, q, scales, pow2=False, stream=None):
+    """moe_fp8_quantize_weights: w [G,N,K] or [N,K] (f32 or bf16) -> q of the same shape (float8_e4m3fn or
+    float8_e5m2), scales [G, ceil(N/128), ceil(K/128)] (or without G) f32."""
+    ty = _Types.ready()
+    *G, N, K = w.shape
+    if len(G) > 1:
+        raise ValueError("w: [G, N, K] or [N, K] expected")
+    code = _arg("w", w, ty.act, w.shape)
+    dev = w.get_device()
+    fmt = _arg("q", q, ty.fp8, w.shape, dev)
+    _arg("scales", scales, ty.f32, (*G, (N + 127) // 128, (K + 127) // 128), dev)
+    _call(dev, _lib.lib().moe_fp8_quantize_weights, "moe_fp8_quantize_weights", w.data_ptr(), code,
+          G[0] if G else 1, N, K, fmt, int(pow2), q.data_ptr(), scales.data_ptr(), stream=stream)
+
+
+def fp8_gemm(a, a_scales, b, b_scales, out, offsets=None, stream=None):
+    """moe_fp8_gemm: a [M,K] with a_scales [ceil(K/128), M], b [G,N,K] or [N,K] with b_scales
+    [G, ceil(N/128), ceil(K/128)] (or without G) -> out [M,N] (f32 or bf16); offsets [G+1] int32 groups the rows."""
+    ty = _Types.ready()
+    M, K = a.shape
+    *G, N, _ = b.shape
+    if len(G) > 1:
+        raise ValueError("b: [G, N, K] or [N, K] expected")
+    af = _arg("a", a, ty.fp8, (M, K))
+    dev, kb = a.get_device(), (K + 127) // 128
+    bf = _arg("b", b, ty.fp8, (*G, N, K), dev)
+    _arg("a_scales", a_scales, ty.f32, (kb, M), dev)
+    _arg("b_scales", b_scales, ty.f32, (*G, (N + 127) // 128, kb), dev)
+    od = _arg("out", out, ty.act, (M, N), dev)
+    g = G[0] if G else 1
+    if offsets is not None:
+        _arg("offsets", offsets, ty.i32, (g + 1,), dev)
+    _call(dev, _lib.lib().moe_fp8_gemm, "moe_fp8_gemm", M, N, K, g, a.data_ptr(), a_scales.data_ptr(), af,
+          b.data_ptr(), b_scales.data_ptr(), bf, _ptr(offsets), out.data_ptr(), od, stream=stream)
+
+
+def experts(desc, x, w, topk_ids, topk_w, out, ws, shared_gate=None, stream=None):
+    """moe_experts: the layer on a given routing (topk_ids [T,K] int32, topk_w [T,K] f32): permutation, experts,
+    shared expert, combine."""
+    ty = _Types.ready()
+    act = ty.f32 if desc.act_dtype == "f32" else ty.bf16
+    T, H, K = desc.T, desc.H, desc.top_k
+    _arg("x", x, act, (T, H))
+    dev = x.get_device()
+    _arg("out", out, act, (T, H), dev)
+    _arg("topk_ids", topk_ids, ty.i32, (T, K), dev)
+    _arg("topk_w", topk_w, ty.f32, (T, K), dev)
+    if shared_gate is not None:
+        _arg("shared_gate", shared_gate, ty.f32, (T,), dev)
+    _call(dev, _lib.lib().moe_experts, "moe_experts", ctypes.byref(desc.c()), x.data_ptr(), ctypes.byref(w.c()),
+          topk_ids.data_ptr(), topk_w.data_ptr(), _ptr(shared_gate), out.data_ptr(), _ptr(ws), _nbytes(ws),
+          stream=stream)
 
 
 def last_device_status(stream=None) -> int:

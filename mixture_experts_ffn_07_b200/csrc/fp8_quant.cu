@@ -1,0 +1,241 @@
+// Quantisation to block-scaled 8-bit floats (fp8.cuh): activation rows with one scale per 128 values, weight
+// matrices with one scale per 128 x 128 block, and the combine of the 8-bit experts' slot rows.
+#include "fp8.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int kRowThreads = 256;
+constexpr int kTileBlocks = 8;   // blocks of 128 along a row per CTA
+constexpr int kTileRows = 32;    // rows per CTA
+constexpr int kHalfWarps = kRowThreads / 16;
+constexpr int kRowsPerPass = kHalfWarps / kTileBlocks;
+
+struct Eight {
+  float v[8];
+};
+__device__ __forceinline__ Eight load8(const float* p, int left) {
+  Eight r;
+  const float4 a = left > 0 ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  const float4 b = left > 4 ? __ldg(reinterpret_cast<const float4*>(p) + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+  r.v[0] = a.x; r.v[1] = a.y; r.v[2] = a.z; r.v[3] = a.w;
+  r.v[4] = b.x; r.v[5] = b.y; r.v[6] = b.z; r.v[7] = b.w;
+  return r;
+}
+__device__ __forceinline__ Eight load8(const __nv_bfloat16* p, int left) {
+  Eight r;
+  const uint4 a = left > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.v[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
+    r.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+  return r;
+}
+
+__device__ __forceinline__ uint32_t amax_bits(const Eight& x) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x.v[i]) & 0x7fffffffu);
+  return m;
+}
+__device__ __forceinline__ uint2 codes8(const Eight& x, float inv, int fmt) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = fp8_pack2(x.v[2 * i] * inv, x.v[2 * i + 1] * inv, fmt);
+  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// A CTA codes kTileRows rows x kTileBlocks blocks; a half-warp holds one block (eight values a lane), so the
+// block's maximum is four shuffles.  Scales go through shared memory: the output is [block, row], and a CTA
+// writes runs of kTileRows.  C is a multiple of 32, so eight values are all inside the row or all outside.
+template <typename XT>
+__global__ void __launch_bounds__(kRowThreads)
+    fp8_rows_kernel(const XT* __restrict__ x, long long stride, int R, int C, int fmt, int pow2,
+                    uint8_t* __restrict__ q, float* __restrict__ scales) {
+  __shared__ float sc[kTileBlocks][kTileRows + 1];
+  const int hw = threadIdx.x >> 4, hl = threadIdx.x & 15;
+  const int bl = hw % kTileBlocks;
+  const int kb = blockIdx.y * kTileBlocks + bl;
+  const int col = kb * kFp8Block + hl * 8;
+  const int left = C - col;
+  const long long row0 = static_cast<long long>(blockIdx.x) * kTileRows;
+  pdl_trigger();
+  pdl_wait();
+  constexpr int kPasses = kTileRows / kRowsPerPass, kBatch = 4;
+#pragma unroll 1
+  for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
+    if (row0 + p0 * kRowsPerPass >= R) break;
+    Eight v[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const long long r = row0 + (p0 + u) * kRowsPerPass + hw / kTileBlocks;
+      v[u] = load8(x + (r < R ? r * stride + col : 0), r < R ? left : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int lr = (p0 + u) * kRowsPerPass + hw / kTileBlocks;
+      const long long r = row0 + lr;
+      uint32_t m = amax_bits(v[u]);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float scale, inv;
+      fp8_scale(m, fmt, pow2 != 0, scale, inv);
+      if (hl == 0) sc[bl][lr] = scale;
+      if (r < R && left > 0) *reinterpret_cast<uint2*>(q + r * C + col) = codes8(v[u], inv, fmt);
+    }
+  }
+  __syncthreads();
+  const int nkb = (C + kFp8Block - 1) / kFp8Block;
+  for (int i = threadIdx.x; i < kTileBlocks * kTileRows; i += kRowThreads) {
+    const int b = i / kTileRows, r = i % kTileRows;
+    if (blockIdx.y * kTileBlocks + b < nkb && row0 + r < R)
+      scales[static_cast<long long>(blockIdx.y * kTileBlocks + b) * R + row0 + r] = sc[b][r];
+  }
+}
+
+// One CTA per 128 x 128 block of a [G, N, K] stack, its values held in registers between the maximum and the
+// codes, so that they are read once.
+template <typename XT>
+__global__ void __launch_bounds__(kRowThreads)
+    fp8_blocks_kernel(const XT* __restrict__ w, int N, int K, int fmt, int pow2, uint8_t* __restrict__ q,
+                      float* __restrict__ scales) {
+  __shared__ uint32_t part[kRowThreads / 32];
+  const int hw = threadIdx.x >> 4, hl = threadIdx.x & 15;
+  const int kb = blockIdx.x, nb = blockIdx.y;
+  const long long g = blockIdx.z;
+  const int col = kb * kFp8Block + hl * 8;
+  const int left = K - col;
+  pdl_trigger();
+  pdl_wait();
+  constexpr int kRows = kFp8Block / kHalfWarps;
+  Eight v[kRows];
+  uint32_t m = 0;
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const int n = nb * kFp8Block + u * kHalfWarps + hw;
+    v[u] = load8(w + (n < N ? (g * N + n) * K + col : 0), n < N ? left : 0);
+  }
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) m = max(m, amax_bits(v[u]));
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kRowThreads / 32; ++i) m = max(m, part[i]);
+  float scale, inv;
+  fp8_scale(m, fmt, pow2 != 0, scale, inv);
+  if (threadIdx.x == 0) scales[(g * gridDim.y + nb) * gridDim.x + kb] = scale;
+#pragma unroll
+  for (int u = 0; u < kRows; ++u) {
+    const int n = nb * kFp8Block + u * kHalfWarps + hw;
+    if (n < N && left > 0) *reinterpret_cast<uint2*>(q + (g * N + n) * K + col) = codes8(v[u], inv, fmt);
+  }
+}
+
+__device__ __forceinline__ float4 load_slot4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
+__device__ __forceinline__ float4 load_slot4(const __nv_bfloat16* p) {
+  const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
+  return make_float4(bf16_bits_to_f32(a.x & 0xFFFFu), __uint_as_float(a.x & 0xFFFF0000u),
+                     bf16_bits_to_f32(a.y & 0xFFFFu), __uint_as_float(a.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// out[t] = sum_k w[t,k] y[t*K+k] in slot order in f32 (w == nullptr: 1; slots whose expert id is outside [0, E)
+// hold no row and count nothing), + y_shared[t].  Four outputs a thread.
+template <typename T, typename OT>
+__global__ void __launch_bounds__(256)
+    combine_ids_kernel(const T* __restrict__ y, const float* __restrict__ w, const int32_t* __restrict__ ids,
+                       const float* __restrict__ y_shared, long long n4, int K, int E, int H4, OT* __restrict__ out) {
+  pdl_trigger();
+  pdl_wait();
+  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n4; i += step) {
+    const long long t = i / H4;
+    const int c = static_cast<int>(i - t * H4) * 4;
+    const int H = H4 * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = 0; k0 < K; k0 += 8) {
+      float4 v[8];
+      float ww[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const long long p = t * K + k0 + j;
+        const int id = k0 + j < K ? ids[p] : -1;
+        const bool ok = id >= 0 && id < E;
+        ww[j] = ok ? (w ? w[p] : 1.f) : 0.f;
+        v[j] = ok ? load_slot4(y + p * H + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        acc.x += ww[j] * v[j].x;
+        acc.y += ww[j] * v[j].y;
+        acc.z += ww[j] * v[j].z;
+        acc.w += ww[j] * v[j].w;
+      }
+    }
+    if (y_shared) {
+      const float4 s = __ldg(reinterpret_cast<const float4*>(y_shared + t * H + c));
+      acc.x += s.x;
+      acc.y += s.y;
+      acc.z += s.z;
+      acc.w += s.w;
+    }
+    store4(out + t * H + c, acc);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_fp8_rows(const Ctx& c, const void* x, int x_dtype, int64_t stride, int64_t R, int C, int fmt,
+                            bool pow2, void* q, float* scales) {
+  const int nkb = (C + kFp8Block - 1) / kFp8Block;
+  const dim3 grid(static_cast<unsigned>((R + kTileRows - 1) / kTileRows), (nkb + kTileBlocks - 1) / kTileBlocks);
+  KernelScope ks(c, "fp8_quantize");
+  if (x_dtype == MOE_F32)
+    return launch_kernel(c, fp8_rows_kernel<float>, grid, dim3(kRowThreads), 0, static_cast<const float*>(x),
+                         static_cast<long long>(stride), static_cast<int>(R), C, fmt, pow2 ? 1 : 0,
+                         static_cast<uint8_t*>(q), scales);
+  return launch_kernel(c, fp8_rows_kernel<__nv_bfloat16>, grid, dim3(kRowThreads), 0,
+                       static_cast<const __nv_bfloat16*>(x), static_cast<long long>(stride), static_cast<int>(R), C,
+                       fmt, pow2 ? 1 : 0, static_cast<uint8_t*>(q), scales);
+}
+
+cudaError_t launch_fp8_blocks(const Ctx& c, const void* w, int w_dtype, int G, int N, int K, int fmt, bool pow2,
+                              void* q, float* scales) {
+  const dim3 grid((K + kFp8Block - 1) / kFp8Block, (N + kFp8Block - 1) / kFp8Block, G);
+  KernelScope ks(c, "fp8_quantize_weights");
+  if (w_dtype == MOE_F32)
+    return launch_kernel(c, fp8_blocks_kernel<float>, grid, dim3(kRowThreads), 0, static_cast<const float*>(w), N, K,
+                         fmt, pow2 ? 1 : 0, static_cast<uint8_t*>(q), scales);
+  return launch_kernel(c, fp8_blocks_kernel<__nv_bfloat16>, grid, dim3(kRowThreads), 0,
+                       static_cast<const __nv_bfloat16*>(w), N, K, fmt, pow2 ? 1 : 0, static_cast<uint8_t*>(q),
+                       scales);
+}
+
+template <typename T, typename OT>
+static cudaError_t combine_ids_typed(const Ctx& c, const void* y, const float* w, const int32_t* ids, const float* ys,
+                                     long long n4, int K, int E, int H, void* out) {
+  const unsigned grid = static_cast<unsigned>(std::max(1LL, std::min<long long>((n4 + 255) / 256, 16LL * c.num_sms)));
+  KernelScope ks(c, "combine");
+  return launch_kernel(c, combine_ids_kernel<T, OT>, dim3(grid), dim3(256), 0, static_cast<const T*>(y), w, ids, ys, n4,
+                       K, E, H / 4, static_cast<OT*>(out));
+}
+
+cudaError_t launch_combine_ids(const Ctx& c, const void* y_slots, int y_dtype, const float* w, const int32_t* ids,
+                               const float* y_shared, int T, int K, int E, int H, void* out, int dtype) {
+  const long long n4 = static_cast<long long>(T) * (H / 4);
+  if (dtype == MOE_F32) return combine_ids_typed<float, float>(c, y_slots, w, ids, y_shared, n4, K, E, H, out);
+  if (y_dtype == MOE_F32)
+    return combine_ids_typed<float, __nv_bfloat16>(c, y_slots, w, ids, y_shared, n4, K, E, H, out);
+  return combine_ids_typed<__nv_bfloat16, __nv_bfloat16>(c, y_slots, w, ids, y_shared, n4, K, E, H, out);
+}
+
+}  // namespace moe

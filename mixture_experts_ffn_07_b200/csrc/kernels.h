@@ -181,4 +181,60 @@ struct PrefillFront {
 };
 cudaError_t launch_prefill_front(const Ctx& c, const PrefillFront& f);
 
+
+// Expert selection with a balance bias, and its gradient (select.cu).
+struct SelectCfg {
+  int T, E, K;
+  int scoring;      // moe_gating
+  int n_groups, topk_groups;
+  int group_score;  // moe_group_score
+  int renorm;
+  float scale;
+};
+cudaError_t launch_select(const Ctx& c, const void* logits, int logits_dtype, int64_t stride, const float* bias,
+                          const SelectCfg& cfg, int32_t* ids, float* w, float* scores);
+cudaError_t launch_select_backward(const Ctx& c, const void* logits, int logits_dtype, int64_t stride,
+                                   const SelectCfg& cfg, const int32_t* ids, const float* d_w, const float* d_scores,
+                                   void* d_logits);
+
+// Block-scaled 8-bit floats (fp8_quant.cu): rows -> codes [R, C] and scales [ceil(C/128), R]; weight stacks ->
+// codes [G, N, K] and scales [G, ceil(N/128), ceil(K/128)].
+cudaError_t launch_fp8_rows(const Ctx& c, const void* x, int x_dtype, int64_t stride, int64_t R, int C, int fmt,
+                            bool pow2, void* q, float* scales);
+cudaError_t launch_fp8_blocks(const Ctx& c, const void* w, int w_dtype, int G, int N, int K, int fmt, bool pow2,
+                              void* q, float* scales);
+// out[t] = sum_k w[t,k] y_slots[t*K+k] over the slots with an id in [0, E) (w == nullptr: 1), + y_shared[t].
+cudaError_t launch_combine_ids(const Ctx& c, const void* y_slots, int y_dtype, const float* w, const int32_t* ids,
+                               const float* y_shared, int T, int K, int E, int H, void* out, int dtype);
+
+// Grouped product of block-scaled 8-bit floats (fp8_gemm.cu): rows [offsets[g], offsets[g+1]) of A against B0[g]
+// (offsets == nullptr: one group of all rows).
+//  dual = true : h = act(A B0^T) * (A B1^T), coded as e4m3 into out_q [rows, N], out_qs [ceil(N/128), rows]
+//  dual = false: out[dest, n] = scale * (A B0^T)[row, n] in f32 or bf16,
+//                dest = row_map ? row_map[row] : row, scale = row_scale ? row_scale[dest] : 1
+struct Fp8GemmArgs {
+  const void* A;         // codes [rows, K]
+  const float* a_scale;  // [ceil(K/128), a_ld]; row r uses column a_scale_map ? a_scale_map[r] / a_scale_div : r
+  int64_t a_ld;
+  const int32_t* a_scale_map;
+  int a_scale_div;
+  int a_fmt, b_fmt;      // MOE_E4M3 | MOE_E5M2
+  int rows, K, N, G;
+  const void* B0;
+  const void* B1;
+  const float* s0;
+  const float* s1;
+  const int32_t* offsets;
+  bool dual;
+  int act;
+  void* out_q;
+  float* out_qs;
+  float* out_f32;
+  __nv_bfloat16* out_bf16;
+  const int32_t* row_map;
+  const float* row_scale;
+  const char* name;
+};
+cudaError_t launch_fp8_gemm(const Ctx& c, const Fp8GemmArgs& a);
+
 }  // namespace moe

@@ -93,6 +93,9 @@ bool tensor_path(const moe_desc& d) {
   return d.act_dtype == MOE_BF16 && d.w_dtype == MOE_BF16 && d.T >= g_tensor_min_tokens.load();
 }
 
+// 8-bit-float expert weights: tensor-core products of block-scaled operands for every T (fp8_gemm.cu).
+bool fp8_path(const moe_desc& d) { return d.w_dtype == MOE_FP8; }
+
 bool tensor_router(const moe_desc& d) {
   return d.act_dtype == MOE_BF16 && d.router_dtype == MOE_BF16 && d.T >= g_tensor_min_tokens.load() && d.E % 32 == 0;
 }
@@ -104,7 +107,7 @@ bool fused_front(const moe_desc& d) { return tensor_path(d) && tensor_router(d);
 // The whole layer as one cooperative kernel (decode_fused.cu): the streaming
 // path with at most 64 tokens.
 bool fused_decode(const moe_desc& d) {
-  return !tensor_path(d) && d.T >= 1 && d.T <= moe::kMaxDecodeT && d.T * d.top_k <= moe::kMaxDecodePairs;
+  return !tensor_path(d) && !fp8_path(d) && d.T >= 1 && d.T <= moe::kMaxDecodeT && d.T * d.top_k <= moe::kMaxDecodePairs;
 }
 
 // Ranges the router GEMM splits the hidden dimension into, so that small batches
@@ -127,7 +130,7 @@ moe_status check_desc(const moe_desc* d) {
     return MOE_ERR_INVALID_ARG;
   if ((d->act_dtype != MOE_F32 && d->act_dtype != MOE_BF16) ||
       (d->w_dtype != MOE_F32 && d->w_dtype != MOE_BF16 && d->w_dtype != MOE_Q8_0 && d->w_dtype != MOE_Q4_K &&
-       d->w_dtype != MOE_Q4_K_Q6_K) ||
+       d->w_dtype != MOE_Q4_K_Q6_K && d->w_dtype != MOE_FP8) ||
       (d->router_dtype != MOE_F32 && d->router_dtype != MOE_BF16))
     return MOE_ERR_INVALID_ARG;
   if (d->H % 32 || d->I % 32 || d->shared_I % 32) return MOE_ERR_UNSUPPORTED;
@@ -156,7 +159,7 @@ moe::RouteCfg route_cfg(const moe_desc& d) {
 
 struct Layout {
   size_t logits, logit_parts, router_parts, stream_sync, front_hist, ids, w, shared_gate, counts, offsets, sorted_pairs, pair_pos,
-      y_slots, x_perm, h, h_s, y_s, total;
+      y_slots, x_perm, h, h_s, y_s, x_q, x_qs, h_qs, hs_qs, total;
 };
 
 Layout layout_of(const moe_desc& d) {
@@ -168,7 +171,7 @@ Layout layout_of(const moe_desc& d) {
     return o;
   };
   const size_t T = d.T, H = d.H, E = d.E, I = d.I, P = T * d.top_k, Is = d.shared_I;
-  const bool tc = tensor_path(d);
+  const bool tc = tensor_path(d), f8 = fp8_path(d);
   L.logits = take(T * E * 4);
   L.logit_parts = tensor_router(d) ? take(router_ksplit(d) * T * E * 4) : 0;
   L.router_parts = fused_decode(d) ? take(moe::decode_router_parts_floats(d.T, d.H, d.E, shared_gated(d)) * 4) : 0;
@@ -181,11 +184,17 @@ Layout layout_of(const moe_desc& d) {
   L.offsets = take((E + 1) * 4);
   L.sorted_pairs = take(P * 4);
   L.pair_pos = take(P * 4);
-  L.y_slots = take(P * H * 4);
-  L.x_perm = tc && !g_tma_gather.load() ? take(P * H * 2) : 0;
-  L.h = take(P * I * (tc ? 2 : 4));
-  L.h_s = Is ? take(T * Is * (tc ? 2 : 4)) : 0;
+  L.y_slots = take(P * H * (f8 && d.act_dtype == MOE_BF16 ? 2 : 4));
+  L.x_perm = f8 ? take(P * H) : tc && !g_tma_gather.load() ? take(P * H * 2) : 0;
+  L.h = take(P * I * (f8 ? 1 : tc ? 2 : 4));
+  L.h_s = Is ? take(T * Is * (f8 ? 1 : tc ? 2 : 4)) : 0;
   L.y_s = Is ? take(T * H * 4) : 0;
+  if (f8) {  // codes of x, and the scales of x and of the hidden rows (one f32 per 128 values)
+    L.x_q = take(T * H);
+    L.x_qs = take((H + 127) / 128 * T * 4);
+    L.h_qs = take((I + 127) / 128 * P * 4);
+    L.hs_qs = Is ? take((Is + 127) / 128 * T * 4) : 0;
+  }
   L.total = off;
   return L;
 }
@@ -259,6 +268,107 @@ moe_status route_impl(const moe::Ctx& c, const moe_desc& d, const void* x, const
   return MOE_OK;
 }
 
+// x as e4m3 codes and scales in the workspace.
+moe_status fp8_code_x(const moe::Ctx& c, const moe_desc& d, const void* x, void* ws, const Layout& L) {
+  MOE_TRY(moe::launch_fp8_rows(c, x, d.act_dtype, d.H, d.T, d.H, MOE_E4M3, false, at<void>(ws, L.x_q),
+                               at<float>(ws, L.x_qs)));
+  return MOE_OK;
+}
+
+// Routed experts on 8-bit floats; x is coded already.  tw: slot rows in f32 times the routing weight
+// (moe_expert_ffn); without it slot rows in act_dtype for launch_combine_ids.
+moe_status fp8_experts(const moe::Ctx& c, const moe_desc& d, const moe_weights& w, const int32_t* offsets,
+                       const int32_t* sorted_pairs, const float* tw, void* y_slots, void* ws, const Layout& L) {
+  const int P = d.T * d.top_k;
+  uint8_t* xp = at<uint8_t>(ws, L.x_perm);
+  // rows of H bytes, moved as rows of H / 2 two-byte elements
+  MOE_TRY(moe::launch_gather_rows(c, at<__nv_bfloat16>(ws, L.x_q), sorted_pairs, offsets, d.E, d.top_k, P, d.H / 2,
+                                  reinterpret_cast<__nv_bfloat16*>(xp)));
+  moe::Fp8GemmArgs a{};
+  a.A = xp;
+  a.a_scale = at<float>(ws, L.x_qs);
+  a.a_ld = d.T;
+  a.a_scale_map = sorted_pairs;
+  a.a_scale_div = d.top_k;
+  a.a_fmt = a.b_fmt = MOE_E4M3;
+  a.rows = P;
+  a.K = d.H;
+  a.N = d.I;
+  a.G = d.E;
+  a.B0 = w.gate;
+  a.B1 = w.up;
+  a.s0 = static_cast<const float*>(w.gate_scale);
+  a.s1 = static_cast<const float*>(w.up_scale);
+  a.offsets = offsets;
+  a.dual = true;
+  a.act = d.act;
+  a.out_q = at<void>(ws, L.h);
+  a.out_qs = at<float>(ws, L.h_qs);
+  a.name = "expert_gate_up_fp8";
+  MOE_TRY(moe::launch_fp8_gemm(c, a));
+  moe::Fp8GemmArgs b{};
+  b.A = at<void>(ws, L.h);
+  b.a_scale = at<float>(ws, L.h_qs);
+  b.a_ld = P;
+  b.a_fmt = b.b_fmt = MOE_E4M3;
+  b.rows = P;
+  b.K = d.I;
+  b.N = d.H;
+  b.G = d.E;
+  b.B0 = w.down;
+  b.s0 = static_cast<const float*>(w.down_scale);
+  b.offsets = offsets;
+  if (!tw && d.act_dtype == MOE_BF16)
+    b.out_bf16 = static_cast<__nv_bfloat16*>(y_slots);
+  else
+    b.out_f32 = static_cast<float*>(y_slots);
+  b.row_map = sorted_pairs;
+  b.row_scale = tw;
+  b.name = "expert_down_fp8";
+  MOE_TRY(moe::launch_fp8_gemm(c, b));
+  return MOE_OK;
+}
+
+// Shared expert on 8-bit floats (x coded already): y_s [T,H] f32 times the gate.
+moe_status fp8_shared(const moe::Ctx& c, const moe_desc& d, const moe_weights& w, const float* gate, float* y_s,
+                      void* ws, const Layout& L) {
+  moe::Fp8GemmArgs a{};
+  a.A = at<void>(ws, L.x_q);
+  a.a_scale = at<float>(ws, L.x_qs);
+  a.a_ld = d.T;
+  a.a_fmt = a.b_fmt = MOE_E4M3;
+  a.rows = d.T;
+  a.K = d.H;
+  a.N = d.shared_I;
+  a.G = 1;
+  a.B0 = w.sh_gate;
+  a.B1 = w.sh_up;
+  a.s0 = static_cast<const float*>(w.sh_gate_scale);
+  a.s1 = static_cast<const float*>(w.sh_up_scale);
+  a.dual = true;
+  a.act = d.act;
+  a.out_q = at<void>(ws, L.h_s);
+  a.out_qs = at<float>(ws, L.hs_qs);
+  a.name = "shared_gate_up_fp8";
+  MOE_TRY(moe::launch_fp8_gemm(c, a));
+  moe::Fp8GemmArgs b{};
+  b.A = at<void>(ws, L.h_s);
+  b.a_scale = at<float>(ws, L.hs_qs);
+  b.a_ld = d.T;
+  b.a_fmt = b.b_fmt = MOE_E4M3;
+  b.rows = d.T;
+  b.K = d.shared_I;
+  b.N = d.H;
+  b.G = 1;
+  b.B0 = w.sh_down;
+  b.s0 = static_cast<const float*>(w.sh_down_scale);
+  b.out_f32 = y_s;
+  b.row_scale = gate;
+  b.name = "shared_down_fp8";
+  MOE_TRY(moe::launch_fp8_gemm(c, b));
+  return MOE_OK;
+}
+
 // bf16_slots (tensor-core path of moe_layer): the slot rows hold the experts' unweighted outputs in bf16 and
 // the combine applies the routing weights (mlx-native moe_dispatch.rs, moe_weighted_sum_seq_bf16_input);
 // otherwise they hold topk_w-weighted f32 rows, as moe_expert_ffn documents.
@@ -323,14 +433,17 @@ moe_status expert_impl(const moe::Ctx& c, const moe_desc& d, const void* x, cons
   return MOE_OK;
 }
 
-moe_status combine_impl(const moe::Ctx& c, const moe_desc& d, const float* y_slots, const void* x,
-                        const moe_weights& w, const float* shared_gate, void* out, void* ws, const Layout& L,
-                        const float* bf16_slot_weights = nullptr) {
+// The shared expert's rows times the gate, in the workspace; *out = nullptr without a shared expert.
+moe_status shared_impl(const moe::Ctx& c, const moe_desc& d, const void* x, const moe_weights& w,
+                       const float* shared_gate, void* ws, const Layout& L, float** out) {
   float* y_s = nullptr;
   if (d.shared_I > 0) {
     y_s = at<float>(ws, L.y_s);
     const float* gate = shared_gated(d) ? shared_gate : nullptr;
-    if (tensor_path(d)) {
+    if (fp8_path(d)) {  // x is coded already
+      const moe_status st = fp8_shared(c, d, w, gate, y_s, ws, L);
+      if (st != MOE_OK) return st;
+    } else if (tensor_path(d)) {
       __nv_bfloat16* hs = at<__nv_bfloat16>(ws, L.h_s);
       moe::GemmArgs a{};
       a.A = static_cast<const __nv_bfloat16*>(x);
@@ -368,11 +481,47 @@ moe_status combine_impl(const moe::Ctx& c, const moe_desc& d, const float* y_slo
                                       nullptr, d.T, gate, y_s));
     }
   }
+  *out = y_s;
+  return MOE_OK;
+}
+
+moe_status combine_impl(const moe::Ctx& c, const moe_desc& d, const float* y_slots, const void* x,
+                        const moe_weights& w, const float* shared_gate, void* out, void* ws, const Layout& L,
+                        const float* bf16_slot_weights = nullptr) {
+  float* y_s = nullptr;
+  const moe_status st = shared_impl(c, d, x, w, shared_gate, ws, L, &y_s);
+  if (st != MOE_OK) return st;
   if (bf16_slot_weights)
     MOE_TRY(moe::launch_combine_weighted(c, reinterpret_cast<const __nv_bfloat16*>(y_slots), bf16_slot_weights, y_s,
                                          d.T, d.top_k, d.H, out));
   else
     MOE_TRY(moe::launch_combine(c, y_slots, y_s, d.T, d.top_k, d.H, out, d.act_dtype));
+  return MOE_OK;
+}
+
+// Permutation, experts, shared expert and combine on a given routing (moe_experts; every format).
+moe_status experts_impl(const moe::Ctx& c, const moe_desc& d, const void* x, const moe_weights& w, const int32_t* ids,
+                        const float* tw, const float* shared_gate, void* out, void* ws, const Layout& L) {
+  int32_t* offsets = at<int32_t>(ws, L.offsets);
+  int32_t* sorted_pairs = at<int32_t>(ws, L.sorted_pairs);
+  float* y_slots = at<float>(ws, L.y_slots);
+  float* y_s = nullptr;
+  moe_status st;
+  MOE_TRY(moe::launch_permute(c, ids, d.T * d.top_k, d.E, at<int32_t>(ws, L.counts), offsets, sorted_pairs,
+                              at<int32_t>(ws, L.pair_pos)));
+  const bool f8 = fp8_path(d), bf16_slots = tensor_path(d);
+  if (f8) {
+    if ((st = fp8_code_x(c, d, x, ws, L)) != MOE_OK) return st;
+    st = fp8_experts(c, d, w, offsets, sorted_pairs, nullptr, y_slots, ws, L);
+  } else {
+    st = expert_impl(c, d, x, w, offsets, sorted_pairs, tw, y_slots, ws, L, false, bf16_slots);
+  }
+  if (st != MOE_OK) return st;
+  if ((st = shared_impl(c, d, x, w, shared_gate, ws, L, &y_s)) != MOE_OK) return st;
+  // slots: in act_dtype and unweighted (8-bit floats, tensor cores), or f32 and weighted (streaming)
+  const bool weighted = !f8 && !bf16_slots;
+  MOE_TRY(moe::launch_combine_ids(c, y_slots, weighted ? MOE_F32 : d.act_dtype, weighted ? nullptr : tw, ids, y_s, d.T,
+                                  d.top_k, d.E, d.H, out, d.act_dtype));
   return MOE_OK;
 }
 
@@ -391,21 +540,29 @@ bool stream_rows_fit(const moe_desc& d, int inner) {
   return xb <= 65536 && static_cast<long long>(inner) * 4 <= 65536;
 }
 
+// Present and aligned for f32 loads.
+bool aligned_scale(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 moe_status check_expert_weights(const moe_desc& d, const moe_weights* w) {
-  if (!tensor_path(d) && !stream_rows_fit(d, d.I)) return MOE_ERR_UNSUPPORTED;
+  if (!tensor_path(d) && !fp8_path(d) && !stream_rows_fit(d, d.I)) return MOE_ERR_UNSUPPORTED;
   if (!w || !w->gate || !w->up || !w->down) return MOE_ERR_INVALID_ARG;
   if (!aligned16(w->gate) || !aligned16(w->up) || !aligned16(w->down)) return MOE_ERR_INVALID_ARG;
   if (d.w_dtype == MOE_Q8_0 && (!w->gate_scale || !w->up_scale || !w->down_scale)) return MOE_ERR_INVALID_ARG;
+  if (fp8_path(d) && (!aligned_scale(w->gate_scale) || !aligned_scale(w->up_scale) || !aligned_scale(w->down_scale)))
+    return MOE_ERR_INVALID_ARG;
   if (d.w_dtype == MOE_Q4_K_Q6_K && (!w->down_scale || !aligned16(w->down_scale))) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
 moe_status check_shared_weights(const moe_desc& d, const moe_weights* w) {
   if (d.shared_I == 0) return MOE_OK;
-  if (!tensor_path(d) && !stream_rows_fit(d, d.shared_I)) return MOE_ERR_UNSUPPORTED;
+  if (!tensor_path(d) && !fp8_path(d) && !stream_rows_fit(d, d.shared_I)) return MOE_ERR_UNSUPPORTED;
   if (!w || !w->sh_gate || !w->sh_up || !w->sh_down) return MOE_ERR_INVALID_ARG;
   if (!aligned16(w->sh_gate) || !aligned16(w->sh_up) || !aligned16(w->sh_down)) return MOE_ERR_INVALID_ARG;
   if (d.w_dtype == MOE_Q8_0 && (!w->sh_gate_scale || !w->sh_up_scale || !w->sh_down_scale))
+    return MOE_ERR_INVALID_ARG;
+  if (fp8_path(d) &&
+      (!aligned_scale(w->sh_gate_scale) || !aligned_scale(w->sh_up_scale) || !aligned_scale(w->sh_down_scale)))
     return MOE_ERR_INVALID_ARG;
   if (d.w_dtype == MOE_Q4_K_Q6_K && (!w->sh_down_scale || !aligned16(w->sh_down_scale))) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
@@ -538,6 +695,10 @@ moe_status moe_expert_ffn(const moe_desc* d, const void* x, const moe_weights* w
   if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
   moe::Ctx c;
   if (!make_ctx(reinterpret_cast<cudaStream_t>(stream), &c)) return MOE_ERR_CUDA;
+  if (fp8_path(*d)) {
+    if ((st = fp8_code_x(c, *d, x, ws, L)) != MOE_OK) return st;
+    return fp8_experts(c, *d, *w, offsets, sorted_pairs, topk_w, y_slots, ws, L);
+  }
   return expert_impl(c, *d, x, *w, offsets, sorted_pairs, topk_w, y_slots, ws, L);
 }
 
@@ -557,6 +718,7 @@ moe_status moe_combine(const moe_desc* d, const float* y_slots, const void* x, c
   if (ws && !aligned16(ws)) return MOE_ERR_INVALID_ARG;
   moe::Ctx c;
   if (!make_ctx(reinterpret_cast<cudaStream_t>(stream), &c)) return MOE_ERR_CUDA;
+  if (fp8_path(*d) && d->shared_I > 0 && (st = fp8_code_x(c, *d, x, ws, L)) != MOE_OK) return st;
   return combine_impl(c, *d, y_slots, x, *w, shared_gate, out, ws, L);
 }
 
@@ -675,6 +837,7 @@ moe_status moe_layer(const moe_desc* d, const void* x, const moe_weights* w, voi
     return combine_impl(c, *d, y_slots, x, *w, sg, out, ws, L, tw);
   }
   if ((st = route_impl(c, *d, x, *w, logits, parts, ids, tw, sg)) != MOE_OK) return st;
+  if (fp8_path(*d)) return experts_impl(c, *d, x, *w, ids, tw, sg, out, ws, L);
   MOE_TRY(moe::launch_permute(c, ids, d->T * d->top_k, d->E, at<int32_t>(ws, L.counts), offsets, sorted_pairs,
                               at<int32_t>(ws, L.pair_pos)));
   const bool bf16_slots = tensor_path(*d);
@@ -746,6 +909,177 @@ moe_status moe_act_up_backward(int64_t P, int64_t I, int32_t act, const float* g
   moe::Ctx c;
   if (!make_ctx(reinterpret_cast<cudaStream_t>(stream), &c)) return MOE_ERR_CUDA;
   return from_cuda(moe::launch_act_up_backward(c, gate_up, d_h, P, I, act, d_gate_up));
+}
+
+moe_status moe_experts(const moe_desc* d, const void* x, const moe_weights* w, const int32_t* topk_ids,
+                       const float* topk_w, const float* shared_gate, void* out, void* ws, size_t ws_bytes,
+                       moe_stream_t stream) {
+  moe_status st = check_desc(d);
+  if (st != MOE_OK) return st;
+  if (d->T == 0) return MOE_OK;
+  if ((st = check_expert_weights(*d, w)) != MOE_OK) return st;
+  if ((st = check_shared_weights(*d, w)) != MOE_OK) return st;
+  if (!x || !aligned16(x) || !topk_ids || !topk_w || !out || !aligned16(out)) return MOE_ERR_INVALID_ARG;
+  if (shared_gated(*d) && !shared_gate) return MOE_ERR_INVALID_ARG;
+  const size_t xb = static_cast<size_t>(d->T) * d->H * (d->act_dtype == MOE_F32 ? 4 : 2);
+  const size_t pb = static_cast<size_t>(d->T) * d->top_k * 4;
+  if (overlaps(out, xb, x, xb) || overlaps(out, xb, topk_ids, pb) || overlaps(out, xb, topk_w, pb))
+    return MOE_ERR_INVALID_ARG;
+  const Layout L = layout_of(*d);
+  if (!ws || ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (!aligned16(ws)) return MOE_ERR_INVALID_ARG;
+  moe::Ctx c;
+  if (!make_ctx(reinterpret_cast<cudaStream_t>(stream), &c)) return MOE_ERR_CUDA;
+  return experts_impl(c, *d, x, *w, topk_ids, topk_w, shared_gate, out, ws, L);
+}
+
+namespace {
+bool fp8_format(int f) { return f == MOE_E4M3 || f == MOE_E5M2; }
+
+moe_status check_select(const moe_select_desc* d, const void* logits, int64_t stride) {
+  if (!d) return MOE_ERR_INVALID_ARG;
+  if (d->T < 0 || d->T > kMaxT || d->E < 1 || d->E > 256 || d->top_k < 1 || d->top_k > d->E || d->top_k > 32)
+    return MOE_ERR_INVALID_ARG;
+  if (d->scoring != MOE_GATING_SOFTMAX && d->scoring != MOE_GATING_SIGMOID) return MOE_ERR_INVALID_ARG;
+  if (d->group_score != MOE_GROUP_MAX && d->group_score != MOE_GROUP_TOP2) return MOE_ERR_INVALID_ARG;
+  if (d->renormalize != 0 && d->renormalize != 1) return MOE_ERR_INVALID_ARG;
+  if (d->logits_dtype != MOE_F32 && d->logits_dtype != MOE_BF16) return MOE_ERR_INVALID_ARG;
+  if (d->n_groups < 0 || d->n_groups > 32) return MOE_ERR_INVALID_ARG;
+  if (d->n_groups > 1 && (d->E % d->n_groups || d->topk_groups < 1 || d->topk_groups > d->n_groups ||
+                          d->top_k > d->topk_groups * (d->E / d->n_groups)))
+    return MOE_ERR_INVALID_ARG;
+  if (d->T == 0) return MOE_OK;
+  const uintptr_t eb = d->logits_dtype == MOE_F32 ? 4 : 2;
+  if (!logits || reinterpret_cast<uintptr_t>(logits) % eb || stride < d->E || stride > (1LL << 40))
+    return MOE_ERR_INVALID_ARG;
+  return MOE_OK;
+}
+
+moe::SelectCfg select_cfg(const moe_select_desc& d) {
+  moe::SelectCfg c{};
+  c.T = d.T;
+  c.E = d.E;
+  c.K = d.top_k;
+  c.scoring = d.scoring;
+  c.n_groups = d.n_groups > 1 ? d.n_groups : 1;
+  c.topk_groups = d.n_groups > 1 ? d.topk_groups : 1;
+  c.group_score = d.group_score;
+  c.renorm = d.renormalize;
+  c.scale = d.scale;
+  return c;
+}
+
+// Bytes from the first logit of the first row to the last one of the last row.
+size_t logits_bytes(const moe_select_desc& d, int64_t stride) {
+  return (static_cast<size_t>(d.T - 1) * stride + d.E) * (d.logits_dtype == MOE_F32 ? 4 : 2);
+}
+}  // namespace
+
+moe_status moe_select(const moe_select_desc* d, const void* logits, int64_t stride, const float* bias, int32_t* ids,
+                      float* w, float* scores, moe_stream_t stream) {
+  const moe_status st = check_select(d, logits, stride);
+  if (st != MOE_OK || d->T == 0) return st;
+  if (!ids || !w) return MOE_ERR_INVALID_ARG;
+  const size_t nl = logits_bytes(*d, stride), np = static_cast<size_t>(d->T) * d->top_k * 4,
+               ns = static_cast<size_t>(d->T) * d->E * 4;
+  if (overlaps(ids, np, logits, nl) || overlaps(w, np, logits, nl) || overlaps(ids, np, w, np) ||
+      (scores && (overlaps(scores, ns, logits, nl) || overlaps(scores, ns, ids, np) || overlaps(scores, ns, w, np))))
+    return MOE_ERR_INVALID_ARG;
+  moe::Ctx c;
+  if (!make_ctx(reinterpret_cast<cudaStream_t>(stream), &c)) return MOE_ERR_CUDA;
+  return from_cuda(moe::launch_select(c, logits, d->logits_dtype, stride, bias, select_cfg(*d), ids, w, scores));
+}
+
+moe_status moe_select_backward(const moe_select_desc* d, const void* logits, int64_t stride, const int32_t* ids,
+                               const float* d_w, const float* d_scores, void* d_logits, moe_stream_t stream) {
+  const moe_status st = check_select(d, logits, stride);
+  if (st != MOE_OK || d->T == 0) return st;
+  if (!ids || !d_w || !d_logits) return MOE_ERR_INVALID_ARG;
+  const size_t eb = d->logits_dtype == MOE_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(d_logits) % eb) return MOE_ERR_INVALID_ARG;
+  const size_t nl = logits_bytes(*d, stride), np = static_cast<size_t>(d->T) * d->top_k * 4,
+               ns = static_cast<size_t>(d->T) * d->E * 4, no = static_cast<size_t>(d->T) * d->E * eb;
+  if (overlaps(d_logits, no, logits, nl) || overlaps(d_logits, no, ids, np) || overlaps(d_logits, no, d_w, np) ||
+      (d_scores && overlaps(d_logits, no, d_scores, ns)))
+    return MOE_ERR_INVALID_ARG;
+  moe::Ctx c;
+  if (!make_ctx(reinterpret_cast<cudaStream_t>(stream), &c)) return MOE_ERR_CUDA;
+  return from_cuda(moe::launch_select_backward(c, logits, d->logits_dtype, stride, select_cfg(*d), ids, d_w, d_scores,
+                                               d_logits));
+}
+
+moe_status moe_fp8_quantize(const void* x, int32_t x_dtype, int64_t R, int64_t C, int64_t stride, int32_t format,
+                            int32_t pow2_scales, void* q, float* scales, moe_stream_t stream) {
+  if (R < 0 || R > (1 << 25) || C < 0 || C > (1 << 20) || C % 32 || (x_dtype != MOE_F32 && x_dtype != MOE_BF16) ||
+      !fp8_format(format) || (pow2_scales != 0 && pow2_scales != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (R == 0 || C == 0) return MOE_OK;
+  const int64_t eb = x_dtype == MOE_F32 ? 4 : 2;
+  if (!x || !q || !scales || !aligned16(x) || !aligned16(q) || !aligned_scale(scales) || stride < C ||
+      stride > (1LL << 40) || stride * eb % 16)
+    return MOE_ERR_INVALID_ARG;
+  const size_t nx = (static_cast<size_t>(R - 1) * stride + C) * eb, nq = static_cast<size_t>(R) * C,
+               ns = static_cast<size_t>(R) * ((C + 127) / 128) * 4;
+  if (overlaps(q, nq, x, nx) || overlaps(scales, ns, x, nx) || overlaps(scales, ns, q, nq)) return MOE_ERR_INVALID_ARG;
+  moe::Ctx c;
+  if (!make_ctx(reinterpret_cast<cudaStream_t>(stream), &c)) return MOE_ERR_CUDA;
+  return from_cuda(moe::launch_fp8_rows(c, x, x_dtype, stride, R, static_cast<int>(C), format, pow2_scales != 0, q,
+                                        scales));
+}
+
+moe_status moe_fp8_quantize_weights(const void* w, int32_t w_dtype, int64_t G, int64_t N, int64_t K, int32_t format,
+                                    int32_t pow2_scales, void* q, float* scales, moe_stream_t stream) {
+  if (G < 0 || G > 65535 || N < 0 || N > (1 << 22) || K < 0 || K > (1 << 20) || K % 32 ||
+      (w_dtype != MOE_F32 && w_dtype != MOE_BF16) || !fp8_format(format) || (pow2_scales != 0 && pow2_scales != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (G == 0 || N == 0 || K == 0) return MOE_OK;
+  if (!w || !q || !scales || !aligned16(w) || !aligned16(q) || !aligned_scale(scales)) return MOE_ERR_INVALID_ARG;
+  const size_t n = static_cast<size_t>(G) * N * K, nw = n * (w_dtype == MOE_F32 ? 4 : 2),
+               ns = static_cast<size_t>(G) * ((N + 127) / 128) * ((K + 127) / 128) * 4;
+  if (overlaps(q, n, w, nw) || overlaps(scales, ns, w, nw) || overlaps(scales, ns, q, n)) return MOE_ERR_INVALID_ARG;
+  moe::Ctx c;
+  if (!make_ctx(reinterpret_cast<cudaStream_t>(stream), &c)) return MOE_ERR_CUDA;
+  return from_cuda(moe::launch_fp8_blocks(c, w, w_dtype, static_cast<int>(G), static_cast<int>(N), static_cast<int>(K),
+                                          format, pow2_scales != 0, q, scales));
+}
+
+moe_status moe_fp8_gemm(int64_t M, int64_t N, int64_t K, int64_t G, const void* a, const float* a_scales,
+                        int32_t a_format, const void* b, const float* b_scales, int32_t b_format,
+                        const int32_t* offsets, void* out, int32_t out_dtype, moe_stream_t stream) {
+  if (M < 0 || M > (1 << 25) || N < 32 || N > (1 << 20) || N % 32 || K < 32 || K > (1 << 20) || K % 32 || G < 1 ||
+      G > 256 || !fp8_format(a_format) || !fp8_format(b_format) || (out_dtype != MOE_F32 && out_dtype != MOE_BF16) ||
+      (!offsets && G != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  if (!a || !b || !out || !aligned16(a) || !aligned16(b) || !aligned16(out) || !aligned_scale(a_scales) ||
+      !aligned_scale(b_scales))
+    return MOE_ERR_INVALID_ARG;
+  const size_t no = static_cast<size_t>(M) * N * (out_dtype == MOE_F32 ? 4 : 2);
+  const size_t nkb = (K + 127) / 128;
+  if (overlaps(out, no, a, static_cast<size_t>(M) * K) || overlaps(out, no, b, static_cast<size_t>(G) * N * K) ||
+      overlaps(out, no, a_scales, nkb * M * 4) || overlaps(out, no, b_scales, nkb * G * ((N + 127) / 128) * 4))
+    return MOE_ERR_INVALID_ARG;
+  moe::Ctx c;
+  if (!make_ctx(reinterpret_cast<cudaStream_t>(stream), &c)) return MOE_ERR_CUDA;
+  moe::Fp8GemmArgs g{};
+  g.A = a;
+  g.a_scale = a_scales;
+  g.a_ld = M;
+  g.a_fmt = a_format;
+  g.b_fmt = b_format;
+  g.rows = static_cast<int>(M);
+  g.K = static_cast<int>(K);
+  g.N = static_cast<int>(N);
+  g.G = static_cast<int>(G);
+  g.B0 = b;
+  g.s0 = b_scales;
+  g.offsets = offsets;
+  if (out_dtype == MOE_BF16)
+    g.out_bf16 = static_cast<__nv_bfloat16*>(out);
+  else
+    g.out_f32 = static_cast<float*>(out);
+  g.name = "fp8_gemm";
+  return from_cuda(moe::launch_fp8_gemm(c, g));
 }
 
 moe_status moe_q6_k_split(const void* blocks, int64_t rows, int64_t cols, void* q, void* scales,
