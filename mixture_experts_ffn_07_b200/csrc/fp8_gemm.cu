@@ -18,46 +18,44 @@
 //  * warp 2: loads the scales of each k-block, multiplies row and tile scale, into a ring of its own;
 //  * warps 4-11: epilogue; warp w reads TMEM lanes 32 (w % 4) and one half of the columns.
 // Every wait is bounded; on expiry the CTA records MOE_ERR_TIMEOUT, drains and exits.
-#include <cstring>
-
-#include "fp8.cuh"
+#include "fp8_mma.cuh"
 
 namespace moe {
 
 namespace {
 
-constexpr int WM = 128;            // weight rows per tile
-constexpr int KB = 128;            // k-block: values that share a scale, and bytes per shared-memory row
-constexpr int W_BYTES = WM * KB;
 constexpr int BOX = 32;            // token rows per TMA box
-constexpr int MAX_G = 256;
-constexpr int THREADS = 384;
-constexpr int EPI_WARPS = 8;
 constexpr int SLOTS = 8;           // k-blocks of scales in flight
+constexpr int PITCH8 = 144;        // dual: staged bytes per row of codes (128 used)
+constexpr int PITCH16 = 80;        // single: staged bytes per row of 32 bf16 outputs (64 used)
 
 template <bool DUAL, int NT>
 struct Cfg {
   static constexpr int MATS = DUAL ? 2 : 1;
   static constexpr int STAGE_BYTES = MATS * W_BYTES + NT * KB;
-  static constexpr int STAGES = NT == 32 ? (DUAL ? 5 : 9) : (NT == 128 && !DUAL ? 6 : 4);
   static constexpr int ACC = MATS * NT;                      // TMEM columns of one accumulator
-  static constexpr uint32_t TMEM_COLS = 2 * ACC < 32 ? 32 : 2 * ACC;
+  static constexpr int NBUF = 512 / ACC < 8 ? 512 / ACC : 8; // accumulators
+  static constexpr uint32_t TMEM_COLS = NBUF * ACC;
   static constexpr int HALF = NT / 2;                        // columns per epilogue warp
+  static constexpr int X = HALF / 8 < 8 ? HALF / 8 : 8;      // 8-column groups per TMEM load
+  static constexpr int CHUNKS = HALF / (8 * X);
+  static constexpr int SCALE_WARPS = NT > 32 ? 2 : 1;
+  static constexpr int OUT_STAGE = DUAL ? NT * PITCH8 : EPI_WARPS * 16 * PITCH16;
 };
 
-template <bool DUAL, int NT>
+template <bool DUAL, int NT, int STAGES>
 struct Aux {
-  alignas(16) float sc[SLOTS][Cfg<DUAL, NT>::MATS][NT];  // row scale x tile scale
-  alignas(16) float inv[NT];                             // dual: 1 / h scale of each column
-  float red[EPI_WARPS][NT / 2];                          // dual: largest |h| of each warp's columns
-  int dest[2][NT];                                       // single: output row of each column (-1: none)
-  float rscale[2][NT];
-  uint64_t full[Cfg<DUAL, NT>::STAGES];
-  uint64_t empty[Cfg<DUAL, NT>::STAGES];
+  alignas(16) float sc[SLOTS][DUAL ? 2 : 1][NT];  // row scale x tile scale
+  alignas(16) float inv[DUAL ? NT : 4];           // dual: 1 / h scale of each column
+  uint32_t red[DUAL ? EPI_WARPS : 1][NT / 2];     // dual: largest |h| of each warp's columns, as bits
+  int dest[2][DUAL ? 4 : NT];                     // single: output row of each column (-1: none)
+  float rscale[2][DUAL ? 4 : NT];
+  uint64_t full[STAGES];
+  uint64_t empty[STAGES];
   uint64_t sfull[SLOTS];
   uint64_t sempty[SLOTS];
-  uint64_t tfull[2];
-  uint64_t tempty[2];
+  uint64_t tfull[8];
+  uint64_t tempty[8];
   uint64_t done;
   uint32_t tmem_base;
   int abort;
@@ -66,97 +64,49 @@ struct Aux {
   int cnt[MAX_G];
 };
 
+// As many stages as fit beside the rest.
 template <bool DUAL, int NT>
-constexpr size_t smem_bytes() {
-  return 1024 + static_cast<size_t>(Cfg<DUAL, NT>::STAGES) * Cfg<DUAL, NT>::STAGE_BYTES + sizeof(Aux<DUAL, NT>);
-}
+constexpr int kStages = (SMEM_MAX - 1024 - static_cast<int>(sizeof(Aux<DUAL, NT, 16>)) - Cfg<DUAL, NT>::OUT_STAGE) /
+                        Cfg<DUAL, NT>::STAGE_BYTES;
+template <bool DUAL, int NT>
+constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages<DUAL, NT>) * Cfg<DUAL, NT>::STAGE_BYTES +
+                         Cfg<DUAL, NT>::OUT_STAGE + sizeof(Aux<DUAL, NT, kStages<DUAL, NT>>);
 
-struct Params {
-  const int32_t* offsets;
-  int G, rows, N, K, n_tiles;
-  const float* a_scale;         // [nkb, a_ld]
-  long long a_ld;
-  const int32_t* a_scale_map;   // row r uses scale column a_scale_map[r] / a_scale_div
-  int a_scale_div;
-  const float* s0;
-  const float* s1;
-  uint32_t idesc;               // without N
-  int act;
-  uint8_t* out_q;
-  float* out_qs;                // [ceil(N/128), rows]
-  float* out_f32;
-  __nv_bfloat16* out_bf16;
-  const int32_t* row_map;
-  const float* row_scale;
-  int* status;
-  long long wait_limit;
-  int skip_stage;
-};
-
-__device__ __forceinline__ bool wait_cycles(uint64_t* bar, uint32_t parity, long long limit) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity))
-    if (clock64() - t0 > limit) return false;
-  return true;
-}
-
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
-                                            int c2, uint64_t policy) {
+// 16 TMEM lanes x 8 X columns.  Group i of 8 columns: registers 4 i, 4 i + 1 hold columns 2 (lane % 4), + 1 of row
+// lane / 4, registers 4 i + 2, 4 i + 3 the same columns of row lane / 4 + 8.  So a thread needs two of the eight
+// column scales, not all of them (reading 32 lanes x 1 column instead cost one shared load per four products).
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_addr(smem_dst)),
-      "l"(map), "r"(smem_addr(bar)), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
-      : "memory");
-}
-
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                        uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+// Waits for the thread's TMEM loads; names the registers, so that nothing reads them earlier.
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 ::"memory");
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
+}
 
-// acc pair += value pair * scale pair (two f32 FMAs)
-__device__ __forceinline__ void fma2(unsigned long long& acc, uint32_t v0, uint32_t v1, unsigned long long s) {
-  unsigned long long v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(v0), "r"(v1));
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(v), "l"(s));
-}
-__device__ __forceinline__ void split2(unsigned long long v, float& lo, float& hi) {
-  uint32_t a, b;
-  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
-  lo = __uint_as_float(a);
-  hi = __uint_as_float(b);
-}
-
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-  asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
-}
-// Every one of `threads` threads says ok.
-__device__ __forceinline__ bool named_barrier_and(int id, int threads, bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %3, 0;\n\t"
-      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
-      "selp.u32 %0, 1, 0, q;\n\t}\n"
-      : "=r"(r)
-      : "r"(id), "r"(threads), "r"(ok ? 1u : 0u)
-      : "memory");
-  return r != 0;
+// Four 8 x 8 matrices of 16-bit values, transposed: lane l gives the address of column l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
 }
 
 // Rows per tile of a group of cnt rows: the fewest tiles of at most NT rows, evened out to multiples of 16.
@@ -195,22 +145,17 @@ __device__ __forceinline__ Item decode_item(const AuxT& aux, int G, int w) {
   return it;
 }
 
-__device__ __forceinline__ float act_fast(int act, float g) {
-  // e^-g and the quotient in the fast forms (a few ulp of f32): h is coded to 4 bits of precision next
-  if (act == MOE_ACT_SILU) return __fdividef(g, 1.0f + __expf(-g));
-  const float z = 0.7978845608028654f * (g + 0.044715f * g * g * g);
-  return 0.5f * g * (1.0f + tanhf(z));
-}
-
 template <bool DUAL, int NT>
 __global__ void __launch_bounds__(THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapW0,
                     const __grid_constant__ CUtensorMap mapW1, const Params p) {
   using C = Cfg<DUAL, NT>;
-  constexpr int STAGES = C::STAGES;
+  constexpr int STAGES = kStages<DUAL, NT>;
+  constexpr int NBUF = C::NBUF;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  Aux<DUAL, NT>& aux = *reinterpret_cast<Aux<DUAL, NT>*>(smem + STAGES * C::STAGE_BYTES);
+  uint8_t* out_stage = smem + STAGES * C::STAGE_BYTES;
+  Aux<DUAL, NT, STAGES>& aux = *reinterpret_cast<Aux<DUAL, NT, STAGES>*>(out_stage + C::OUT_STAGE);
   volatile int* abort_flag = &aux.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -220,10 +165,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&aux.empty[s], 1);
     }
     for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(&aux.sfull[s], 1);
+      mbar_init(&aux.sfull[s], C::SCALE_WARPS);
       mbar_init(&aux.sempty[s], EPI_WARPS);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < NBUF; ++b) {
       mbar_init(&aux.tfull[b], 1);
       mbar_init(&aux.tempty[b], EPI_WARPS);
     }
@@ -286,8 +231,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   const long long limit = p.wait_limit;
 
   if (warp < 4) {
-    // 128 x 56 + 256 x 224 = 384 x 168 registers, what the CTA was launched with
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0) {
       if (lane == 0) {
         // -------------------------------------------------------- TMA producer
@@ -309,7 +252,8 @@ __global__ void __launch_bounds__(THREADS, 1)
               continue;
             }
             uint8_t* st = smem + s * C::STAGE_BYTES;
-            mbar_arrive_expect_tx(&aux.full[s], C::MATS * W_BYTES + boxes * BOX * KB);
+            const int bytes = C::MATS * W_BYTES + boxes * BOX * KB;
+            mbar_arrive_expect_tx(&aux.full[s], bytes);
             tma_load_3d(st, &mapW0, &aux.full[s], kb * KB, it.wt * WM, it.g, pol_w);
             if (DUAL) tma_load_3d(st + W_BYTES, &mapW1, &aux.full[s], kb * KB, it.wt * WM, it.g, pol_w);
             for (int b = 0; b < boxes; ++b)
@@ -334,8 +278,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t idesc = p.idesc | ((n16 >> 3) << 17);
           for (int kb = 0; kb < nkb; ++kb, ++kbg) {
             const int s = kbg % STAGES;
-            const int buf = kbg & 1;
-            if (!mbar_wait_bounded(&aux.tempty[buf], ((kbg >> 1) & 1u) ^ 1u, limit, abort_flag) ||
+            const int buf = kbg % NBUF;
+            if (!mbar_wait_bounded(&aux.tempty[buf], ((kbg / NBUF) & 1u) ^ 1u, limit, abort_flag) ||
                 !mbar_wait_bounded(&aux.full[s], (kbg / STAGES) & 1u, limit, abort_flag)) {
               ok = false;
               break;
@@ -359,9 +303,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         umma_commit(&aux.done);  // every MMA issued above completes before TMEM is released
         wait_cycles(&aux.done, 0, limit);
       }
-    } else if (warp == 2) {
-      // ---------------------------------------------------------- scales
-      constexpr int PER = NT / 32;
+    } else if (warp - 2 < C::SCALE_WARPS) {
+      // ---------------------------------------------------------- scales: warp 2 + i has the i-th part of the columns.
+      // AHEAD k-blocks are in flight per warp (a load takes about 1000 cycles, a k-block about 500).
+      constexpr int PER = NT / 32 / C::SCALE_WARPS, AHEAD = 4;
+      const int col0 = (warp - 2) * 32 * PER + lane;
       uint32_t kbg = 0;
       bool ok = true;
       for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
@@ -369,13 +315,13 @@ __global__ void __launch_bounds__(THREADS, 1)
         int at[PER];
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-          const int r = it.row0 + min(lane + 32 * j, it.n - 1);
+          const int r = it.row0 + min(col0 + 32 * j, it.n - 1);
           int col = p.a_scale_map ? p.a_scale_map[r] / p.a_scale_div : r;
           col = min(max(col, 0), static_cast<int>(p.a_ld) - 1);
           at[j] = col;
         }
         const long long sb = (static_cast<long long>(it.g) * p.n_tiles + it.wt) * nkb;
-        float v[2][PER], t0[2], t1[2];
+        float v[AHEAD][PER], t0[AHEAD], t1[AHEAD];
         auto load = [&](int kb, int b) {
           const int k = min(kb, nkb - 1);
 #pragma unroll
@@ -383,11 +329,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           t0[b] = __ldg(p.s0 + sb + k);
           t1[b] = DUAL ? __ldg(p.s1 + sb + k) : 0.f;
         };
-        load(0, 0);
-        load(1, 1);
-        for (int kb0 = 0; kb0 < nkb && ok; kb0 += 2) {
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < AHEAD; ++b) load(b, b);
+        for (int kb0 = 0; kb0 < nkb && ok; kb0 += AHEAD) {
+#pragma unroll
+          for (int b = 0; b < AHEAD; ++b) {
             if (kb0 + b >= nkb) break;
             const int slot = kbg % SLOTS;
             const bool got = mbar_wait_bounded(&aux.sempty[slot], ((kbg / SLOTS) & 1u) ^ 1u, limit, abort_flag);
@@ -397,10 +343,10 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
-              aux.sc[slot][0][lane + 32 * j] = v[b][j] * t0[b];
-              if (DUAL) aux.sc[slot][C::MATS - 1][lane + 32 * j] = v[b][j] * t1[b];
+              aux.sc[slot][0][col0 + 32 * j] = v[b][j] * t0[b];
+              if (DUAL) aux.sc[slot][C::MATS - 1][col0 + 32 * j] = v[b][j] * t1[b];
             }
-            load(kb0 + b + 2, b);
+            load(kb0 + b + AHEAD, b);
             __syncwarp();
             if (lane == 0) mbar_arrive(&aux.sfull[slot]);
             ++kbg;
@@ -409,18 +355,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     // -------------------------------------------------------------- epilogue
-    constexpr int HALF = C::HALF;
-    constexpr int CH = 16;  // columns per TMEM load
+    constexpr int HALF = C::HALF, X = C::X, CHUNKS = C::CHUNKS, MATS = C::MATS;
+    constexpr int STEPS = MATS * CHUNKS * 2;  // TMEM loads per k-block: (matrix, column chunk, 16-lane half)
     const int ew = warp - 4;
     const int q = warp & 3, half = ew >> 2;
     const int et = threadIdx.x - 128;  // thread of the epilogue
+    const int lr = lane >> 2, lc = 2 * (lane & 3);  // row and column inside an 8 x 8 block
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     uint32_t kbg = 0;
     int parity = 0;
     for (int w = blockIdx.x; w < total; w += gridDim.x, parity ^= 1) {
       const Item it = decode_item<NT>(aux, p.G, w);
+      const int wt = it.wt;
       const int n16 = (it.n + 15) & ~15;
       if (!DUAL) {  // output row and scale of each column
         for (int c = et; c < NT; c += EPI_WARPS * 32) {
@@ -439,37 +386,42 @@ __global__ void __launch_bounds__(THREADS, 1)
           aux.rscale[parity][c] = rs;
         }
       }
-      unsigned long long acc[C::MATS][HALF / 2];
+      // acc[m][chunk][half of the lanes][2 i + b]: columns 8 (chunk X + i) + lc, + 1 of row 16 half + 8 b + lr
+      unsigned long long acc[MATS][CHUNKS][2][2 * X];
 #pragma unroll
-      for (int m = 0; m < C::MATS; ++m)
+      for (int m = 0; m < MATS; ++m)
 #pragma unroll
-        for (int j = 0; j < HALF / 2; ++j) acc[m][j] = 0ull;
+        for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+          for (int j = 0; j < 2 * X; ++j) acc[m][c][0][j] = acc[m][c][1][j] = 0ull;
       bool ok = true;
       for (int kb = 0; kb < nkb; ++kb, ++kbg) {
-        const int slot = kbg % SLOTS, buf = kbg & 1;
+        const int slot = kbg % SLOTS, buf = kbg % NBUF;
         const bool got = mbar_wait_bounded(&aux.sfull[slot], (kbg / SLOTS) & 1u, limit, abort_flag) &&
-                         mbar_wait_bounded(&aux.tfull[buf], (kbg >> 1) & 1u, limit, abort_flag);
+                         mbar_wait_bounded(&aux.tfull[buf], (kbg / NBUF) & 1u, limit, abort_flag);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t tb = tmem_base + lane_base + buf * C::ACC + half * HALF;
+        if (half * HALF < n16) {  // warp-uniform
+          const uint32_t tb = tmem_base + lane_base + buf * C::ACC + half * HALF;
+          unsigned long long sc[X];
 #pragma unroll
-        for (int c = 0; c < HALF; c += CH) {
-          if (half * HALF + c >= n16) break;  // warp-uniform
-          uint32_t v[C::MATS][CH];
+          for (int st = 0; st < STEPS; ++st) {
+            const int m = st / (2 * CHUNKS), c = st / 2 % CHUNKS, r = st & 1;
+            uint32_t v[4 * X];
+            tmem_ld_16x256b(tb + (static_cast<uint32_t>(16 * r) << 16) + m * NT + c * 8 * X, v);
+            if (r == 0) {
 #pragma unroll
-          for (int m = 0; m < C::MATS; ++m) tmem_ld_32x32b_x16(tb + m * NT + c, v[m]);
-          tmem_ld_wait();
+              for (int i = 0; i < X; ++i)
+                sc[i] = *reinterpret_cast<const unsigned long long*>(&aux.sc[slot][m][half * HALF + 8 * (c * X + i) + lc]);
+            }
+            tmem_wait(v);
 #pragma unroll
-          for (int m = 0; m < C::MATS; ++m) {
-            const ulonglong2* s2 = reinterpret_cast<const ulonglong2*>(&aux.sc[slot][m][half * HALF + c]);
-#pragma unroll
-            for (int j = 0; j < CH / 4; ++j) {
-              const ulonglong2 s = s2[j];
-              fma2(acc[m][c / 2 + 2 * j], v[m][4 * j], v[m][4 * j + 1], s.x);
-              fma2(acc[m][c / 2 + 2 * j + 1], v[m][4 * j + 2], v[m][4 * j + 3], s.y);
+            for (int i = 0; i < X; ++i) {
+              fma2(acc[m][c][r][2 * i], v[4 * i], v[4 * i + 1], sc[i]);
+              fma2(acc[m][c][r][2 * i + 1], v[4 * i + 2], v[4 * i + 3], sc[i]);
             }
           }
         }
@@ -482,67 +434,137 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       // uniform over the epilogue: either every warp has all k-blocks or the tile is dropped; also orders dest
       if (!named_barrier_and(1, EPI_WARPS * 32, ok)) break;
-      const int n = it.wt * WM + q * 32 + lane;  // this thread's weight row
       if (DUAL) {
-        float mx = 0.f;
-        uint32_t keep = 0;
+        // h = act(g) * u in place of g, and the largest |h| of each of the thread's 2 X columns over its four rows
+        const ActCoef ac = act_coef(p.act);
+        uint32_t mx[2 * X];
 #pragma unroll
-        for (int j = 0; j < HALF; j += 2) {
-          float g0, g1, u0, u1;
-          split2(acc[0][j / 2], g0, g1);
-          split2(acc[C::MATS - 1][j / 2], u0, u1);
-          const float h0 = act_fast(p.act, g0) * u0, h1 = act_fast(p.act, g1) * u1;
-          acc[0][j / 2] = static_cast<unsigned long long>(__float_as_uint(h0)) |
-                          (static_cast<unsigned long long>(__float_as_uint(h1)) << 32);
-          const uint32_t m0 = __reduce_max_sync(0xffffffffu, __float_as_uint(h0) & 0x7fffffffu);
-          const uint32_t m1 = __reduce_max_sync(0xffffffffu, __float_as_uint(h1) & 0x7fffffffu);
-          if (lane == (j & 31)) keep = m0;
-          if (lane == (j & 31) + 1) keep = m1;
-          if ((j & 31) == 30 || j == HALF - 2)
-            if (lane <= (j & 31) + 1) aux.red[ew][(j & ~31) + lane] = __uint_as_float(keep);
+        for (int i = 0; i < X; ++i) {
+          mx[2 * i] = mx[2 * i + 1] = 0;
+#pragma unroll
+          for (int rb = 0; rb < 4; ++rb) {
+            float g0, g1, u0, u1;
+            split2(acc[0][0][rb >> 1][2 * i + (rb & 1)], g0, g1);
+            split2(acc[MATS - 1][0][rb >> 1][2 * i + (rb & 1)], u0, u1);
+            const float h0 = act_fast(ac, g0) * u0, h1 = act_fast(ac, g1) * u1;
+            acc[0][0][rb >> 1][2 * i + (rb & 1)] = join2(h0, h1);
+            mx[2 * i] = max(mx[2 * i], __float_as_uint(h0) & 0x7fffffffu);
+            mx[2 * i + 1] = max(mx[2 * i + 1], __float_as_uint(h1) & 0x7fffffffu);
+          }
         }
-        (void)mx;
+        // over the warp's 32 rows: halve the columns a lane keeps while exchanging with lanes 16, 8, 4 away
+        int base = 0;
+#pragma unroll
+        for (int b = 0; b < 3; ++b) {
+          constexpr int N0 = 2 * X;
+          const int keep = N0 >> (b + 1);
+          const int o = 16 >> b;
+          const bool upper = lane & o;
+          if (keep > 0) {
+#pragma unroll
+            for (int j = 0; j < keep; ++j) {
+              const uint32_t give = upper ? mx[j] : mx[j + keep], take = upper ? mx[j + keep] : mx[j];
+              mx[j] = max(take, __shfl_xor_sync(0xffffffffu, give, o));
+            }
+            base += upper ? keep : 0;
+          } else {
+            mx[0] = max(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
+          }
+        }
+        constexpr int LEFT = 2 * X / 8 > 1 ? 2 * X / 8 : 1;
+#pragma unroll
+        for (int j = 0; j < LEFT; ++j) {
+          const int k = base + j;  // the thread's column k: group k / 2, parity k % 2
+          aux.red[ew][8 * (k >> 1) + lc + (k & 1)] = mx[j];
+        }
         named_barrier(2 + half, 128);
         if (et - half * 128 < HALF) {
           const int c = et - half * 128;
           uint32_t m = 0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) m = max(m, __float_as_uint(aux.red[half * 4 + i][c]));
+          for (int i = 0; i < 4; ++i) m = max(m, aux.red[half * 4 + i][c]);
           float scale, inv;
           fp8_scale(m, MOE_E4M3, false, scale, inv);
           const int col = half * HALF + c;
           aux.inv[col] = inv;
-          if (col < it.n) p.out_qs[static_cast<long long>(it.wt) * p.rows + it.row0 + col] = scale;
+          if (col < it.n) p.out_qs[static_cast<long long>(wt) * p.rows + it.row0 + col] = scale;
         }
         named_barrier(2 + half, 128);
-        if (n < p.N) {
-          uint8_t* o = p.out_q + static_cast<long long>(it.row0 + half * HALF) * p.N + n;
+        uint8_t* stage = out_stage + half * HALF * PITCH8;
 #pragma unroll
-          for (int j = 0; j < HALF; j += 2) {
-            if (half * HALF + j < it.n) {
-              float h0, h1;
-              split2(acc[0][j / 2], h0, h1);
-              const uint32_t code = fp8_pack2(h0 * aux.inv[half * HALF + j], h1 * aux.inv[half * HALF + j + 1], MOE_E4M3);
-              o[static_cast<long long>(j) * p.N] = static_cast<uint8_t>(code);
-              if (half * HALF + j + 1 < it.n) o[static_cast<long long>(j + 1) * p.N] = static_cast<uint8_t>(code >> 8);
-            }
+        for (int i = 0; i < X; ++i) {
+          const float2 inv = *reinterpret_cast<const float2*>(&aux.inv[half * HALF + 8 * i + lc]);
+          uint8_t* o = stage + (8 * i + lc) * PITCH8 + q * 32 + lr;
+#pragma unroll
+          for (int rb = 0; rb < 4; ++rb) {
+            float h0, h1;
+            split2(acc[0][0][rb >> 1][2 * i + (rb & 1)], h0, h1);
+            const uint32_t code = fp8_pack2(h0 * inv.x, h1 * inv.y, MOE_E4M3);
+            o[8 * rb] = static_cast<uint8_t>(code);
+            o[8 * rb + PITCH8] = static_cast<uint8_t>(code >> 8);
           }
         }
-      } else if (n < p.N) {
+        named_barrier(2 + half, 128);
+        // whole rows of 128 codes: eight lanes a row
+        const int ch = et & 7;
+        if (wt * WM + ch * 16 < p.N) {
 #pragma unroll
-        for (int j = 0; j < HALF; j += 2) {
-          float y0, y1;
-          split2(acc[0][j / 2], y0, y1);
-          const int c = half * HALF + j;
-          const int d0 = aux.dest[parity][c], d1 = aux.dest[parity][c + 1];
-          y0 *= aux.rscale[parity][c];
-          y1 *= aux.rscale[parity][c + 1];
-          if (p.out_bf16) {
-            if (d0 >= 0) p.out_bf16[static_cast<long long>(d0) * p.N + n] = __float2bfloat16_rn(y0);
-            if (d1 >= 0) p.out_bf16[static_cast<long long>(d1) * p.N + n] = __float2bfloat16_rn(y1);
-          } else {
-            if (d0 >= 0) p.out_f32[static_cast<long long>(d0) * p.N + n] = y0;
-            if (d1 >= 0) p.out_f32[static_cast<long long>(d1) * p.N + n] = y1;
+          for (int c0 = 0; c0 < HALF; c0 += 16) {
+            const int c = c0 + ((et & 127) >> 3);
+            const int col = half * HALF + c;
+            if (col < it.n)
+              *reinterpret_cast<uint4*>(p.out_q + static_cast<long long>(it.row0 + col) * p.N + wt * WM + ch * 16) =
+                  *reinterpret_cast<const uint4*>(stage + c * PITCH8 + ch * 16);
+          }
+        }
+      } else if (wt * WM + q * 32 < p.N) {  // N is a multiple of 32: the warp's rows are all inside or all outside
+        if (p.out_bf16) {
+          // 16 columns at a time through the warp's staging rows: [column][32 rows] bf16
+          uint8_t* stage = out_stage + ew * 16 * PITCH16;
+          const uint32_t st_addr = smem_addr(stage) + (lane & 7) * PITCH16 + (lane >> 3) * 16;
+          const int ch = lane & 3;
+#pragma unroll
+          for (int i = 0; i < CHUNKS * X; i += 2) {
+            if (half * HALF + 8 * i >= it.n) break;  // warp-uniform
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint32_t pk[4];
+              const int col = half * HALF + 8 * (i + e) + lc;
+              const float s0 = aux.rscale[parity][col], s1 = aux.rscale[parity][col + 1];
+#pragma unroll
+              for (int rb = 0; rb < 4; ++rb) {
+                float y0, y1;
+                split2(acc[0][(i + e) / X][rb >> 1][2 * ((i + e) % X) + (rb & 1)], y0, y1);
+                const __nv_bfloat162 t = __floats2bfloat162_rn(y0 * s0, y1 * s1);
+                pk[rb] = *reinterpret_cast<const uint32_t*>(&t);
+              }
+              stmatrix_x4_trans(st_addr + e * 8 * PITCH16, pk[0], pk[1], pk[2], pk[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int c = 8 * e + lr;
+              const int d = aux.dest[parity][half * HALF + 8 * i + c];
+              const uint4 v = *reinterpret_cast<const uint4*>(stage + c * PITCH16 + ch * 16);
+              if (d >= 0)
+                *reinterpret_cast<uint4*>(p.out_bf16 + static_cast<long long>(d) * p.N + wt * WM + q * 32 + ch * 8) = v;
+            }
+            __syncwarp();
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < CHUNKS * X; ++i) {
+            const int col = half * HALF + 8 * i + lc;
+            const int d0 = aux.dest[parity][col], d1 = aux.dest[parity][col + 1];
+            const float s0 = aux.rscale[parity][col], s1 = aux.rscale[parity][col + 1];
+            float* o = p.out_f32 + wt * WM + q * 32 + lr;
+#pragma unroll
+            for (int rb = 0; rb < 4; ++rb) {
+              float y0, y1;
+              split2(acc[0][i / X][rb >> 1][2 * (i % X) + (rb & 1)], y0, y1);
+              if (d0 >= 0) o[static_cast<long long>(d0) * p.N + 8 * rb] = y0 * s0;
+              if (d1 >= 0) o[static_cast<long long>(d1) * p.N + 8 * rb] = y1 * s1;
+            }
           }
         }
       }
@@ -559,79 +581,16 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ------------------------------------------------------------------ host side
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(f);
-  }
-  return fn;
-}
-
-// Bytes [groups, rows, cols] read in boxes of box_rows x 128 bytes, 128-byte swizzle; what lies outside a group's
-// rows or columns reads as zero.
-bool make_map(CUtensorMap* m, const void* base, uint64_t groups, uint64_t rows, uint64_t cols, uint32_t box_rows) {
-  EncodeTiledFn enc = encode_fn();
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {cols, rows, groups};
-  const cuuint64_t strides[2] = {cols, rows * cols};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(KB), box_rows, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, groups ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <bool DUAL, int NT>
 cudaError_t launch_typed(const Ctx& c, const Fp8GemmArgs& a) {
   CUtensorMap mA, m0, m1;
-  if (!make_map(&mA, a.A, 0, static_cast<uint64_t>(a.rows), static_cast<uint64_t>(a.K), BOX) ||
-      !make_map(&m0, a.B0, static_cast<uint64_t>(a.G), static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.K), WM))
-    return cudaErrorInvalidValue;
-  if (DUAL) {
-    if (!make_map(&m1, a.B1, static_cast<uint64_t>(a.G), static_cast<uint64_t>(a.N), static_cast<uint64_t>(a.K), WM))
-      return cudaErrorInvalidValue;
-  } else {
-    m1 = m0;
-  }
-  Params p{};
-  p.offsets = a.offsets;
-  p.G = a.G;
-  p.rows = a.rows;
-  p.N = a.N;
-  p.K = a.K;
-  p.n_tiles = (a.N + WM - 1) / WM;
-  p.a_scale = a.a_scale;
-  p.a_ld = a.a_ld;
-  p.a_scale_map = a.a_scale_map;
-  p.a_scale_div = a.a_scale_div > 0 ? a.a_scale_div : 1;
-  p.s0 = a.s0;
-  p.s1 = a.s1;
-  // kind::f8f6f4 instruction descriptor: D f32, formats of the M operand (weights) and the N operand (rows), M
-  p.idesc = (1u << 4) | (static_cast<uint32_t>(a.b_fmt == MOE_E5M2) << 7) |
-            (static_cast<uint32_t>(a.a_fmt == MOE_E5M2) << 10) | (static_cast<uint32_t>(WM >> 4) << 24);
-  p.act = a.act;
-  p.out_q = static_cast<uint8_t*>(a.out_q);
-  p.out_qs = a.out_qs;
-  p.out_f32 = a.out_f32;
-  p.out_bf16 = a.out_bf16;
-  p.row_map = a.row_map;
-  p.row_scale = a.row_scale;
-  p.status = c.status;
-  p.wait_limit = c.wait_limit;
-  p.skip_stage = c.skip_stage;
+  if (!make_maps(a, BOX, &mA, &m0, &m1)) return cudaErrorInvalidValue;
+  const Params p = make_params(c, a, a.b_fmt, a.a_fmt, WM);
   const long long tiles = a.rows / 16 < a.G ? a.rows : a.rows / 16 + a.G;  // no fewer than there can be
   const int grid = static_cast<int>(std::max(1LL, std::min<long long>(c.num_sms, tiles * p.n_tiles)));
   auto kern = fp8_gemm_kernel<DUAL, NT>;
-  constexpr size_t smem = smem_bytes<DUAL, NT>();
-  static_assert(smem <= 232448, "shared memory of one block");
+  constexpr size_t smem = kSmem<DUAL, NT>;
+  static_assert(smem <= SMEM_MAX && kStages<DUAL, NT> >= 3 && kStages<DUAL, NT> <= 16, "stages");
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   KernelScope ks(c, a.name ? a.name : "fp8_gemm");
@@ -643,10 +602,13 @@ cudaError_t launch_typed(const Ctx& c, const Fp8GemmArgs& a) {
 cudaError_t launch_fp8_gemm(const Ctx& c, const Fp8GemmArgs& a) {
   if (a.rows <= 0 || a.G <= 0) return cudaSuccess;
   if (a.G > MAX_G || a.N % 32 || a.K % 32 || a.N <= 0 || a.K <= 0) return cudaErrorInvalidValue;
-  const double per_group = static_cast<double>(a.rows) / std::min(a.G, a.rows);
-  const bool small = per_group <= 16.0;
-  if (a.dual) return small ? launch_typed<true, 32>(c, a) : launch_typed<true, 128>(c, a);
-  return small ? launch_typed<false, 32>(c, a) : launch_typed<false, 256>(c, a);
+  // Mean rows of a group, of the groups that can hold any.  Measured crossovers with fp8_gemm_rows.cu (64 experts, K and N
+  // of 1024 and 2048): gate/up 62 us here and 71 us there at 48 rows, 76 and 72 us at 64; down 37 and 35 us at 16,
+  // 41 and 35 us at 24.
+  const double rows = static_cast<double>(a.rows) / std::min(a.G, a.rows);
+  if (rows > (a.dual ? 48.0 : 16.0)) return launch_fp8_rows_gemm(c, a);
+  if (!a.dual) return launch_typed<false, 32>(c, a);
+  return rows > 16.0 ? launch_typed<true, 64>(c, a) : launch_typed<true, 32>(c, a);
 }
 
 }  // namespace moe
