@@ -13,7 +13,7 @@ streams; it computes nothing here.
 from __future__ import annotations
 
 import ctypes
-from dataclasses import dataclass, fields
+from dataclasses import dataclass
 
 from . import _lib
 from ._lib import (MOE_ACT_GELU_TANH, MOE_ACT_SILU, MOE_BF16, MOE_ERR_CUDA, MOE_ERR_DEVICE_INDEX,  # noqa: F401
@@ -96,7 +96,10 @@ class Weights:
     sh_down_scale: object = None
 
     def c(self) -> _lib.MoeWeights:
-        return _lib.MoeWeights(*[_ptr(getattr(self, f.name)) for f in fields(self)])
+        return _lib.MoeWeights(*[None if t is None else t.data_ptr() for t in (
+            self.router, self.router_bias, self.gate, self.up, self.down, self.sh_gate, self.sh_up, self.sh_down,
+            self.sh_gate_w, self.gate_scale, self.up_scale, self.down_scale, self.sh_gate_scale, self.sh_up_scale,
+            self.sh_down_scale)])
 
 
 def _ptr(t):
@@ -207,12 +210,13 @@ def q6_k_srow_bytes(cols: int) -> int:
 class _Types:
     """moe_dtype of each torch dtype that an argument of the calls below may have (made at the first call, so that
     importing the package does not import torch)."""
-    i32 = f32 = act = fp8 = None
+    i32 = f32 = act = bf16 = fp8 = torch = None
 
     @classmethod
     def ready(cls):
         if cls.i32 is None:
             import torch
+            cls.torch = torch
             cls.i32 = {torch.int32: 0}
             cls.f32 = {torch.float32: MOE_F32}
             cls.act = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
@@ -246,13 +250,15 @@ def _row_stride(name, t):
 
 def _call(device, fn, name, *args, stream):
     """One library call with `device` current, on `stream` (default: that device's current stream)."""
-    import torch
-    prev = torch.cuda.current_device()
-    if prev == device:
-        check(fn(*args, _stream(stream)), name)
-        return
-    with torch.cuda.device(device):
-        check(fn(*args, _stream(stream)), name)
+    torch = _Types.torch
+    if torch._C._cuda_getDevice() != device:
+        with torch.cuda.device(device):
+            return _call(device, fn, name, *args, stream=stream)
+    # the raw handle: building a torch.cuda.Stream to read it from takes as long as the launch
+    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
+    code = fn(*args, raw)
+    if code != MOE_OK:
+        raise MoeError(code, name)
 
 
 def select(desc, logits, ids, w, bias=None, scores=None, stream=None):

@@ -11,12 +11,16 @@
 // row (decode) to a few hundred.  A weight tile's scale is then one number per k-block, a row's scale one number
 // per accumulator column, and 128 outputs that share an h scale are the 128 TMEM lanes of one tile.
 //
-// A k-block of 128 is four MMAs of K = 32 into one of two TMEM accumulators; the epilogue warps read each
-// finished k-block out of TMEM and add it, scaled, to f32 registers while the next one runs.
-//  * warp 0: TMA producer (weight tiles 128 x 128 bytes, token tiles in boxes of 32 rows, 128-byte swizzle);
+// A k-block of 128 is four MMAs of K = 32 into one of the TMEM accumulators; the epilogue warps read each finished
+// k-block out of TMEM and add it, scaled, to f32 registers while the next ones run.
+//  * warp 0: TMA producer (weight tiles 128 x 128 bytes; token rows in boxes of 32, 128-byte swizzle, or, for the
+//    routed gate/up of small batches, gathered row by row straight from the tokens with tile::gather4);
 //  * warp 1: allocates TMEM, issues tcgen05.mma kind::f8f6f4 from one lane;
-//  * warp 2: loads the scales of each k-block, multiplies row and tile scale, into a ring of its own;
+//  * warps 2 and 3: load the scales of each k-block, multiply row and tile scale, into a ring;
 //  * warps 4-11: epilogue; warp w reads TMEM lanes 32 (w % 4) and one half of the columns.
+//
+// Few items (one decoded token: experts x weight tiles, fewer than SMs) split K over a cluster of up to eight CTAs:
+// each sums its k-blocks, leaves the sums in its shared memory, and the first CTA adds them in rank order.
 // Every wait is bounded; on expiry the CTA records MOE_ERR_TIMEOUT, drains and exits.
 #include "fp8_mma.cuh"
 
@@ -25,7 +29,6 @@ namespace moe {
 namespace {
 
 constexpr int BOX = 32;            // token rows per TMA box
-constexpr int SLOTS = 8;           // k-blocks of scales in flight
 constexpr int PITCH8 = 144;        // dual: staged bytes per row of codes (128 used)
 constexpr int PITCH16 = 80;        // single: staged bytes per row of 32 bf16 outputs (64 used)
 
@@ -40,20 +43,27 @@ struct Cfg {
   static constexpr int X = HALF / 8 < 8 ? HALF / 8 : 8;      // 8-column groups per TMEM load
   static constexpr int CHUNKS = HALF / (8 * X);
   static constexpr int SCALE_WARPS = NT > 32 ? 2 : 1;
+  // Ring of scales.  The scale warps write a k-block's slot after its stage came free, that is after the MMA STAGES
+  // k-blocks earlier, which the epilogue's reads of the k-block NBUF before that one (values and scales) precede: a
+  // slot STAGES + NBUF k-blocks old is read, and the ring needs no barriers of its own.
+  static constexpr int SLOTS = NT == 32 ? 32 : 16;
   static constexpr int OUT_STAGE = DUAL ? NT * PITCH8 : EPI_WARPS * 16 * PITCH16;
+};
+
+struct Item {
+  int g, wt, row0, n;  // group, weight tile, first row, rows
+  bool alone;          // the group has one token tile: its weights are read once
 };
 
 template <bool DUAL, int NT, int STAGES>
 struct Aux {
-  alignas(16) float sc[SLOTS][DUAL ? 2 : 1][NT];  // row scale x tile scale
+  alignas(16) float sc[Cfg<DUAL, NT>::SLOTS][DUAL ? 2 : 1][NT];  // row scale x tile scale
   alignas(16) float inv[DUAL ? NT : 4];           // dual: 1 / h scale of each column
   uint32_t red[DUAL ? EPI_WARPS : 1][NT / 2];     // dual: largest |h| of each warp's columns, as bits
   int dest[2][DUAL ? 4 : NT];                     // single: output row of each column (-1: none)
   float rscale[2][DUAL ? 4 : NT];
   uint64_t full[STAGES];
   uint64_t empty[STAGES];
-  uint64_t sfull[SLOTS];
-  uint64_t sempty[SLOTS];
   uint64_t tfull[8];
   uint64_t tempty[8];
   uint64_t done;
@@ -62,6 +72,7 @@ struct Aux {
   int item_off[MAX_G + 1];
   int row_off[MAX_G];
   int cnt[MAX_G];
+  Item first;  // this CTA's first item
 };
 
 // As many stages as fit beside the rest.
@@ -109,18 +120,20 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                : "memory");
 }
 
-// Rows per tile of a group of cnt rows: the fewest tiles of at most NT rows, evened out to multiples of 16.
-template <int NT>
-__device__ __forceinline__ int rows_per_tile(int cnt) {
+// Item `local` of group g: its tiles of NT rows, every one against the same weight tile before the next weight tile.
+template <int NT, typename AuxT>
+__device__ __forceinline__ Item item_at(const AuxT& aux, int g, int local) {
+  Item it;
+  it.g = g;
+  const int cnt = aux.cnt[g];
   const int tiles = (cnt + NT - 1) / NT;
-  const int per = ((cnt + tiles - 1) / max(tiles, 1) + 15) & ~15;
-  return min(NT, max(per, 16));
+  it.alone = tiles == 1;
+  it.wt = it.alone ? local : local / tiles;
+  const int tt = local - it.wt * tiles;
+  it.row0 = aux.row_off[g] + tt * NT;
+  it.n = min(NT, cnt - tt * NT);
+  return it;
 }
-
-struct Item {
-  int g, wt, row0, n;  // group, weight tile, first row, rows
-  bool alone;          // the group has one token tile: its weights are read once
-};
 template <int NT, typename AuxT>
 __device__ __forceinline__ Item decode_item(const AuxT& aux, int G, int w) {
   int lo = 0, hi = G - 1;
@@ -131,18 +144,39 @@ __device__ __forceinline__ Item decode_item(const AuxT& aux, int G, int w) {
     else
       hi = mid - 1;
   }
-  Item it;
-  it.g = lo;
-  const int cnt = aux.cnt[lo];
-  const int per = rows_per_tile<NT>(cnt);
-  const int tiles = (cnt + per - 1) / per;
-  const int local = w - aux.item_off[lo];
-  it.wt = local / tiles;
-  const int tt = local - it.wt * tiles;
-  it.row0 = aux.row_off[lo] + tt * per;
-  it.n = min(per, cnt - tt * per);
-  it.alone = tiles == 1;
-  return it;
+  return item_at<NT>(aux, lo, w - aux.item_off[lo]);
+}
+
+// The two halves of a barrier over every thread of the cluster (whole warps); they order the shared-memory accesses
+// around them.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// What every role but the epilogue does at the end of an item whose k-blocks a cluster shares.
+__device__ __forceinline__ void pass_item(bool split) {
+  if (split) {
+    cluster_arrive();
+    cluster_wait();
+    cluster_arrive();
+    cluster_wait();
+  }
+}
+__device__ __forceinline__ unsigned long long ld_cluster(uint32_t cluster_address) {
+  unsigned long long v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_address) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t cluster_id() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t clusters() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%nclusterid.x;" : "=r"(r));
+  return r;
 }
 
 template <bool DUAL, int NT>
@@ -152,21 +186,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   using C = Cfg<DUAL, NT>;
   constexpr int STAGES = kStages<DUAL, NT>;
   constexpr int NBUF = C::NBUF;
+  constexpr int SLOTS = C::SLOTS;
+  static_assert(SLOTS >= STAGES + NBUF, "ring of scales");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* out_stage = smem + STAGES * C::STAGE_BYTES;
   Aux<DUAL, NT, STAGES>& aux = *reinterpret_cast<Aux<DUAL, NT, STAGES>*>(out_stage + C::OUT_STAGE);
   volatile int* abort_flag = &aux.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool split = p.split > 1;
+  const int rank = split ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first = split ? cluster_id() : blockIdx.x, step = split ? clusters() : gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&aux.full[s], 1);
+      mbar_init(&aux.full[s], 1 + C::SCALE_WARPS);
       mbar_init(&aux.empty[s], 1);
-    }
-    for (int s = 0; s < SLOTS; ++s) {
-      mbar_init(&aux.sfull[s], C::SCALE_WARPS);
-      mbar_init(&aux.sempty[s], EPI_WARPS);
     }
     for (int b = 0; b < NBUF; ++b) {
       mbar_init(&aux.tfull[b], 1);
@@ -184,26 +219,30 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(&aux.tmem_base, C::TMEM_COLS);
     tmem_relinquish();
   }
+  // p.early (the down projection behind its own gate/up, whose launch waited for everything before it before it let
+  // this one start): the offsets and the weights are there already, so the weights' copies start at once, while
+  // the last CTAs of the launch before still run; what that launch writes is read after pdl_wait.
+  if (!p.early) pdl_wait();
   pdl_trigger();
-  pdl_wait();
-  for (int g = threadIdx.x; g < p.G; g += THREADS) {
-    const int o0 = p.offsets ? p.offsets[g] : 0;
-    const int o1 = p.offsets ? p.offsets[g + 1] : p.rows;
-    // a group's rows stay inside the tensor, whatever the offsets hold
-    const int r0 = min(max(o0, 0), p.rows), r1 = min(max(o1, r0), p.rows);
-    if (r0 != o0 || r1 != o1) record_status(p.status, MOE_ERR_DEVICE_INDEX);
-    aux.row_off[g] = r0;
-    aux.cnt[g] = r1 - r0;
-  }
-  __syncthreads();
-  if (warp == 0) {  // exclusive scan of the work items per group; lane owns groups [8 lane, 8 lane + 8)
-    int v[8], local = 0;
+  if (warp == 0) {  // rows and work items of each group; lane owns groups [8 lane, 8 lane + 8)
+    int off[9], v[8], local = 0;
+#pragma unroll
+    for (int i = 0; i < 9; ++i) {
+      const int g = lane * 8 + i;
+      off[i] = p.offsets && g <= p.G ? p.offsets[g] : (g == 0 ? 0 : p.rows);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int g = lane * 8 + i;
-      const int cnt = g < p.G ? aux.cnt[g] : 0;
-      const int per = rows_per_tile<NT>(cnt);
-      v[i] = (cnt + per - 1) / per * p.n_tiles;
+      v[i] = 0;
+      if (g < p.G) {
+        // a group's rows stay inside the tensor, whatever the offsets hold
+        const int r0 = min(max(off[i], 0), p.rows), r1 = min(max(off[i + 1], r0), p.rows);
+        if (r0 != off[i] || r1 != off[i + 1]) record_status(p.status, MOE_ERR_DEVICE_INDEX);
+        aux.row_off[g] = r0;
+        aux.cnt[g] = r1 - r0;
+        v[i] = (r1 - r0 + NT - 1) / NT * p.n_tiles;
+      }
       local += v[i];
     }
     int incl = local;
@@ -217,6 +256,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < 8; ++i) {
       const int g = lane * 8 + i;
       if (g < p.G) aux.item_off[g] = run;
+      if (run <= first && first < run + v[i]) aux.first = item_at<NT>(aux, g, first - run);
       run += v[i];
     }
     if (lane == 31) aux.item_off[p.G] = incl;
@@ -227,120 +267,179 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   const uint32_t tmem_base = aux.tmem_base;
   const int total = aux.item_off[p.G];
-  const int nkb = (p.K + KB - 1) / KB;
+  const int nkb_all = (p.K + KB - 1) / KB;
+  // this CTA's k-blocks
+  const int kb_lo = rank * p.kb_per, kb_hi = min(nkb_all, kb_lo + p.kb_per);
   const long long limit = p.wait_limit;
+  // With split every role passes two cluster barriers per item (before and after the first CTA's reads), whether its
+  // CTA still works or has given up.
 
-  if (warp < 4) {
-    if (warp == 0) {
-      if (lane == 0) {
-        // -------------------------------------------------------- TMA producer
-        uint32_t kbg = 0, outstanding = 0, out_phase = 0;
-        bool skipped = false;
-        const uint64_t pol_first = l2_policy_evict_first(), pol_normal = l2_policy_evict_normal(),
-                       pol_last = l2_policy_evict_last();
-        for (int w = blockIdx.x; w < total && !*abort_flag; w += gridDim.x) {
-          const Item it = decode_item<NT>(aux, p.G, w);
-          const int boxes = (it.n + BOX - 1) / BOX;
-          const uint64_t pol_w = it.alone ? pol_first : pol_normal;
-          for (int kb = 0; kb < nkb; ++kb, ++kbg) {
-            const int s = kbg % STAGES;
-            const uint32_t ph = (kbg / STAGES) & 1u;
-            if (!mbar_wait_bounded(&aux.empty[s], ph ^ 1u, limit, abort_flag)) break;
-            outstanding &= ~(1u << s);
-            if (p.skip_stage && !skipped && blockIdx.x == 0) {  // debug: leave this stage unfilled
-              skipped = true;
-              continue;
+  if (warp == 0) {
+    // ---------------------------------------------------------- TMA producer (whole warp: lane l gathers rows
+    // [4 l, 4 l + 4) of a tile, lane 0 does the rest)
+    uint32_t kbg = 0, outstanding = 0, out_phase = 0;
+    bool ok = true;
+    const uint64_t pol_first = l2_policy_evict_first(), pol_normal = l2_policy_evict_normal(),
+                   pol_last = l2_policy_evict_last();
+    for (int w = first; w < total; w += step) {
+      ok = ok && !__shfl_sync(0xffffffffu, *abort_flag, 0);
+      if (ok) {
+        const Item it = w == first ? aux.first : decode_item<NT>(aux, p.G, w);
+        const int quads = (it.n + 3) / 4, boxes = (it.n + BOX - 1) / BOX;
+        const uint64_t pol_w = it.alone ? pol_first : pol_normal;
+        int tok[4] = {0, 0, 0, 0};
+        if (p.gather && lane < quads)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int t = p.a_scale_map[it.row0 + min(4 * lane + j, it.n - 1)] / p.a_scale_div;
+            tok[j] = min(max(t, 0), static_cast<int>(p.a_ld) - 1);
+          }
+        const int bytes = C::MATS * W_BYTES + (p.gather ? quads * 4 * KB : boxes * BOX * KB);
+        int done = 0;  // k-blocks of this item already requested
+        if (w == first) {
+          // The first item's first stages are free, and a lane fills each: waiting for and arriving on a barrier takes
+          // a lane a few hundred cycles, which one lane would spend stage after stage.  Weights before rows, whose
+          // indexes (gathered) or values (early) are still on their way.
+          const int fill = min(STAGES, kb_hi - kb_lo);
+          const bool mine = lane < fill && !(p.skip_stage && lane == 0 && blockIdx.x == 0);  // debug: one stage unfilled
+          uint8_t* st = smem + lane * C::STAGE_BYTES;
+          const int x = (kb_lo + lane) * KB;
+          if (mine) {
+            mbar_arrive_expect_tx(&aux.full[lane], bytes);
+            tma_load_3d(st, &mapW0, &aux.full[lane], x, it.wt * WM, it.g, pol_w);
+            if (DUAL) tma_load_3d(st + W_BYTES, &mapW1, &aux.full[lane], x, it.wt * WM, it.g, pol_w);
+          }
+          if (p.early) pdl_wait();
+          if (p.gather) {
+            for (int b = 0; b < quads; ++b) {
+              int t[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) t[j] = __shfl_sync(0xffffffffu, tok[j], b);
+              if (mine)
+                tma_gather4(st + C::MATS * W_BYTES + b * 4 * KB, &mapA, &aux.full[lane], x, t[0], t[1], t[2], t[3],
+                            pol_last);
             }
-            uint8_t* st = smem + s * C::STAGE_BYTES;
-            const int bytes = C::MATS * W_BYTES + boxes * BOX * KB;
+          } else if (mine) {
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d_hint(st + C::MATS * W_BYTES + b * BOX * KB, &mapA, &aux.full[lane], x, it.row0 + b * BOX,
+                               pol_last);
+          }
+          __syncwarp();
+          outstanding = (1u << fill) - 1u;
+          done = fill;
+        }
+        for (int n = done; n < kb_hi - kb_lo; ++n) {
+          const int kb = kb_lo + n;
+          const uint32_t k = kbg + n;
+          const int s = k % STAGES;
+          const uint32_t ph = (k / STAGES) & 1u;
+          int got = 1;
+          if (lane == 0) got = mbar_wait_bounded(&aux.empty[s], ph ^ 1u, limit, abort_flag);
+          if (!__shfl_sync(0xffffffffu, got, 0)) break;
+          outstanding &= ~(1u << s);
+          uint8_t* st = smem + s * C::STAGE_BYTES;
+          uint8_t* sa = st + C::MATS * W_BYTES;
+          if (lane == 0) {
             mbar_arrive_expect_tx(&aux.full[s], bytes);
             tma_load_3d(st, &mapW0, &aux.full[s], kb * KB, it.wt * WM, it.g, pol_w);
             if (DUAL) tma_load_3d(st + W_BYTES, &mapW1, &aux.full[s], kb * KB, it.wt * WM, it.g, pol_w);
-            for (int b = 0; b < boxes; ++b)
-              tma_load_2d_hint(st + C::MATS * W_BYTES + b * BOX * KB, &mapA, &aux.full[s], kb * KB, it.row0 + b * BOX,
-                               pol_last);
-            outstanding |= 1u << s;
-            out_phase = (out_phase & ~(1u << s)) | (ph << s);
           }
-        }
-        if (*abort_flag)  // let issued copies land before the CTA exits
-          for (int s = 0; s < STAGES; ++s)
-            if (outstanding & (1u << s)) wait_cycles(&aux.full[s], (out_phase >> s) & 1u, limit);
-      }
-    } else if (warp == 1) {
-      if (lane == 0) {
-        // -------------------------------------------------------- MMA issuer
-        uint32_t kbg = 0;
-        bool ok = true;
-        for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
-          const Item it = decode_item<NT>(aux, p.G, w);
-          const uint32_t n16 = (it.n + 15) & ~15;
-          const uint32_t idesc = p.idesc | ((n16 >> 3) << 17);
-          for (int kb = 0; kb < nkb; ++kb, ++kbg) {
-            const int s = kbg % STAGES;
-            const int buf = kbg % NBUF;
-            if (!mbar_wait_bounded(&aux.tempty[buf], ((kbg / NBUF) & 1u) ^ 1u, limit, abort_flag) ||
-                !mbar_wait_bounded(&aux.full[s], (kbg / STAGES) & 1u, limit, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t st = smem_addr(smem + s * C::STAGE_BYTES);
-            const uint64_t tdesc = sw128_kmajor_desc(st + C::MATS * W_BYTES);
-#pragma unroll
-            for (int m = 0; m < C::MATS; ++m) {
-              const uint64_t wdesc = sw128_kmajor_desc(st + m * W_BYTES);
-              const uint32_t d = tmem_base + buf * C::ACC + m * NT;
-#pragma unroll
-              for (int kk = 0; kk < KB / 32; ++kk)
-                umma_f8(d, wdesc + static_cast<uint64_t>(kk * 2), tdesc + static_cast<uint64_t>(kk * 2), idesc,
-                        kk > 0 ? 1u : 0u);
-            }
-            umma_commit(&aux.empty[s]);
-            umma_commit(&aux.tfull[buf]);
+          __syncwarp();
+          if (p.gather) {
+            if (lane < quads)
+              tma_gather4(sa + lane * 4 * KB, &mapA, &aux.full[s], kb * KB, tok[0], tok[1], tok[2], tok[3], pol_last);
+          } else if (lane < boxes) {
+            tma_load_2d_hint(sa + lane * BOX * KB, &mapA, &aux.full[s], kb * KB, it.row0 + lane * BOX, pol_last);
           }
+          outstanding |= 1u << s;
+          out_phase = (out_phase & ~(1u << s)) | (ph << s);
         }
-        umma_commit(&aux.done);  // every MMA issued above completes before TMEM is released
-        wait_cycles(&aux.done, 0, limit);
+        kbg += kb_hi - kb_lo;
       }
-    } else if (warp - 2 < C::SCALE_WARPS) {
-      // ---------------------------------------------------------- scales: warp 2 + i has the i-th part of the columns.
-      // AHEAD k-blocks are in flight per warp (a load takes about 1000 cycles, a k-block about 500).
-      constexpr int PER = NT / 32 / C::SCALE_WARPS, AHEAD = 4;
-      const int col0 = (warp - 2) * 32 * PER + lane;
-      uint32_t kbg = 0;
-      bool ok = true;
-      for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
-        const Item it = decode_item<NT>(aux, p.G, w);
+      pass_item(split);
+    }
+    if (lane == 0 && *abort_flag)  // let issued copies land before the CTA exits
+      for (int s = 0; s < STAGES; ++s)
+        if (outstanding & (1u << s)) wait_cycles(&aux.full[s], (out_phase >> s) & 1u, limit);
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- MMA issuer (one lane)
+    uint32_t kbg = 0;
+    bool ok = true;
+    for (int w = first; w < total; w += step) {
+      if (lane == 0 && ok) {
+        const Item it = w == first ? aux.first : decode_item<NT>(aux, p.G, w);
+        const uint32_t n16 = (it.n + 15) & ~15;
+        const uint32_t idesc = p.idesc | ((n16 >> 3) << 17);
+        for (int kb = kb_lo; kb < kb_hi; ++kb, ++kbg) {
+          const int s = kbg % STAGES;
+          const int buf = kbg % NBUF;
+          if (!mbar_wait_bounded(&aux.tempty[buf], ((kbg / NBUF) & 1u) ^ 1u, limit, abort_flag) ||
+              !mbar_wait_bounded(&aux.full[s], (kbg / STAGES) & 1u, limit, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = smem_addr(smem + s * C::STAGE_BYTES);
+          const uint64_t tdesc = sw128_kmajor_desc(st + C::MATS * W_BYTES);
+#pragma unroll
+          for (int m = 0; m < C::MATS; ++m) {
+            const uint64_t wdesc = sw128_kmajor_desc(st + m * W_BYTES);
+            const uint32_t d = tmem_base + buf * C::ACC + m * NT;
+#pragma unroll
+            for (int kk = 0; kk < KB / 32; ++kk)
+              umma_f8(d, wdesc + static_cast<uint64_t>(kk * 2), tdesc + static_cast<uint64_t>(kk * 2), idesc,
+                      kk > 0 ? 1u : 0u);
+          }
+          umma_commit(&aux.empty[s]);
+          umma_commit(&aux.tfull[buf]);
+        }
+      }
+      pass_item(split);
+    }
+    if (lane == 0) {
+      umma_commit(&aux.done);  // every MMA issued above completes before TMEM is released
+      wait_cycles(&aux.done, 0, limit);
+    }
+  } else if (warp < 4) {
+    // ---------------------------------------------------------- scales: warp 2 + i has the i-th part of the columns.
+    // AHEAD k-blocks are in flight per warp (a load takes about 1000 cycles).
+    constexpr int PER = NT / 32 / C::SCALE_WARPS, AHEAD = 4;
+    const int col0 = (warp - 2) * 32 * PER + lane;
+    uint32_t kbg = 0;
+    bool ok = warp - 2 < C::SCALE_WARPS;
+    if (p.early) pdl_wait();
+    for (int w = first; w < total; w += step) {
+      if (ok) {
+        const Item it = w == first ? aux.first : decode_item<NT>(aux, p.G, w);
         int at[PER];
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
           const int r = it.row0 + min(col0 + 32 * j, it.n - 1);
-          int col = p.a_scale_map ? p.a_scale_map[r] / p.a_scale_div : r;
-          col = min(max(col, 0), static_cast<int>(p.a_ld) - 1);
-          at[j] = col;
+          const int col = p.a_scale_map ? p.a_scale_map[r] / p.a_scale_div : r;
+          at[j] = min(max(col, 0), static_cast<int>(p.a_ld) - 1);
         }
-        const long long sb = (static_cast<long long>(it.g) * p.n_tiles + it.wt) * nkb;
+        const long long sb = (static_cast<long long>(it.g) * p.n_tiles + it.wt) * nkb_all;
         float v[AHEAD][PER], t0[AHEAD], t1[AHEAD];
         auto load = [&](int kb, int b) {
-          const int k = min(kb, nkb - 1);
+          const int k = min(kb, nkb_all - 1);
 #pragma unroll
           for (int j = 0; j < PER; ++j) v[b][j] = __ldg(p.a_scale + k * p.a_ld + at[j]);
           t0[b] = __ldg(p.s0 + sb + k);
           t1[b] = DUAL ? __ldg(p.s1 + sb + k) : 0.f;
         };
 #pragma unroll
-        for (int b = 0; b < AHEAD; ++b) load(b, b);
-        for (int kb0 = 0; kb0 < nkb && ok; kb0 += AHEAD) {
+        for (int b = 0; b < AHEAD; ++b) load(kb_lo + b, b);
+        for (int kb0 = kb_lo; kb0 < kb_hi && ok; kb0 += AHEAD) {
 #pragma unroll
-          for (int b = 0; b < AHEAD; ++b) {
-            if (kb0 + b >= nkb) break;
-            const int slot = kbg % SLOTS;
-            const bool got = mbar_wait_bounded(&aux.sempty[slot], ((kbg / SLOTS) & 1u) ^ 1u, limit, abort_flag);
+          for (int b = 0; b < AHEAD; ++b) {  // unrolled, so that a scale in flight is never moved between registers
+            if (kb0 + b >= kb_hi) break;
+            const int s = kbg % STAGES;
+            const bool got = mbar_wait_bounded(&aux.empty[s], ((kbg / STAGES) & 1u) ^ 1u, limit, abort_flag);
             if (!__all_sync(0xffffffffu, got)) {
               ok = false;
               break;
             }
+            const int slot = kbg % SLOTS;
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
               aux.sc[slot][0][col0 + 32 * j] = v[b][j] * t0[b];
@@ -348,14 +447,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             load(kb0 + b + AHEAD, b);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&aux.sfull[slot]);
+            if (lane == 0) mbar_arrive(&aux.full[s]);
             ++kbg;
           }
         }
       }
+      pass_item(split);
     }
   } else {
-    // -------------------------------------------------------------- epilogue
+    // ---------------------------------------------------------- epilogue
     constexpr int HALF = C::HALF, X = C::X, CHUNKS = C::CHUNKS, MATS = C::MATS;
     constexpr int STEPS = MATS * CHUNKS * 2;  // TMEM loads per k-block: (matrix, column chunk, 16-lane half)
     const int ew = warp - 4;
@@ -365,8 +465,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t lane_base = static_cast<uint32_t>(q * 32) << 16;
     uint32_t kbg = 0;
     int parity = 0;
-    for (int w = blockIdx.x; w < total; w += gridDim.x, parity ^= 1) {
-      const Item it = decode_item<NT>(aux, p.G, w);
+    bool alive = true;
+    if (p.early) pdl_wait();
+    for (int w = first; w < total; w += step, parity ^= 1) {
+      const Item it = w == first ? aux.first : decode_item<NT>(aux, p.G, w);
       const int wt = it.wt;
       const int n16 = (it.n + 15) & ~15;
       if (!DUAL) {  // output row and scale of each column
@@ -394,12 +496,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int c = 0; c < CHUNKS; ++c)
 #pragma unroll
           for (int j = 0; j < 2 * X; ++j) acc[m][c][0][j] = acc[m][c][1][j] = 0ull;
-      bool ok = true;
-      for (int kb = 0; kb < nkb; ++kb, ++kbg) {
+      bool ok = alive;
+      for (int kb = kb_lo; kb < kb_hi && ok; ++kb, ++kbg) {
         const int slot = kbg % SLOTS, buf = kbg % NBUF;
-        const bool got = mbar_wait_bounded(&aux.sfull[slot], (kbg / SLOTS) & 1u, limit, abort_flag) &&
-                         mbar_wait_bounded(&aux.tfull[buf], (kbg / NBUF) & 1u, limit, abort_flag);
-        if (!__all_sync(0xffffffffu, got)) {
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&aux.tfull[buf], (kbg / NBUF) & 1u, limit, abort_flag))) {
           ok = false;
           break;
         }
@@ -427,13 +527,72 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&aux.tempty[buf]);
-          mbar_arrive(&aux.sempty[slot]);
-        }
+        if (lane == 0) mbar_arrive(&aux.tempty[buf]);
       }
       // uniform over the epilogue: either every warp has all k-blocks or the tile is dropped; also orders dest
-      if (!named_barrier_and(1, EPI_WARPS * 32, ok)) break;
+      alive = named_barrier_and(1, EPI_WARPS * 32, ok);
+      if (split) {
+        // The k-ranges' sums, left in each CTA's first stages (every copy into them has been used) and added in rank
+        // order.  Distributed shared memory passes about 20 bytes a cycle, so only columns in use are read; a plain
+        // product is added and written by all the CTAs, each a part of the values, h by the first one, which needs
+        // whole columns for their scales.
+        constexpr int VALS = MATS * CHUNKS * 4 * X, PITCH = EPI_WARPS * 32;
+        static_assert(VALS * PITCH * 8 <= STAGES * C::STAGE_BYTES, "partial sums");
+        unsigned long long* mine = reinterpret_cast<unsigned long long*>(smem) + et;
+        unsigned long long* flat = &acc[0][0][0][0];  // value j: columns 8 ((j / 2) % X) + lc, + 1 of a row
+#pragma unroll
+        for (int j = 0; j < VALS; ++j) mine[j * PITCH] = flat[j];
+        cluster_arrive();
+        cluster_wait();
+        if (DUAL) {
+          if (rank == 0)
+            for (int r = 1; r < p.split; ++r) {
+              const uint32_t from = cluster_addr(mine, r);
+              unsigned long long v[VALS];
+#pragma unroll
+              for (int j = 0; j < VALS; ++j) {
+                v[j] = 0;
+                if (half * HALF + 8 * (j / 2 % X) + lc < it.n) v[j] = ld_cluster(from + j * PITCH * 8);
+              }
+#pragma unroll
+              for (int j = 0; j < VALS; ++j) flat[j] = add2(flat[j], v[j]);
+            }
+        } else if (alive) {
+#pragma unroll
+          for (int j = 0; j < VALS; ++j) {
+            const int col = half * HALF + 8 * (j / 2 % X) + lc;
+            const int n = wt * WM + q * 32 + 16 * (j / (2 * X) % 2) + 8 * (j & 1) + lr;
+            if (j % p.split != rank || col >= it.n || n >= p.N) continue;
+            unsigned long long v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+              if (r < p.split) v[r] = ld_cluster(cluster_addr(mine, r) + j * PITCH * 8);
+#pragma unroll
+            for (int r = 1; r < 8; ++r)
+              if (r < p.split) v[0] = add2(v[0], v[r]);
+            float y[2];
+            split2(v[0], y[0], y[1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int d = aux.dest[parity][col + e];
+              if (d < 0) continue;
+              const float o = y[e] * aux.rscale[parity][col + e];
+              if (p.out_bf16)
+                p.out_bf16[static_cast<long long>(d) * p.N + n] = __float2bfloat16_rn(o);
+              else
+                p.out_f32[static_cast<long long>(d) * p.N + n] = o;
+            }
+          }
+        }
+        // the next item's copies into those stages come after these generic accesses
+        fence_proxy_async_smem();
+        cluster_arrive();
+        if (!DUAL || rank > 0 || !alive) {
+          cluster_wait();
+          continue;
+        }
+      }
+      if (!alive) break;
       if (DUAL) {
         // h = act(g) * u in place of g, and the largest |h| of each of the thread's 2 X columns over its four rows
         const ActCoef ac = act_coef(p.act);
@@ -568,6 +727,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       }
+      if (split) {
+        __syncwarp();
+        cluster_wait();
+      }
     }
   }
 
@@ -578,37 +741,68 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_dealloc(tmem_base, C::TMEM_COLS);
   }
   if (threadIdx.x == 0 && aux.abort) record_status(p.status, MOE_ERR_TIMEOUT);
+  if (p.early) pdl_wait();  // complete only after the launch before
 }
 
 // ------------------------------------------------------------------ host side
+// How many CTAs share an item's k-blocks (1 to 8, of two k-blocks at least each): as many as there are SMs for.
+void set_split(const Ctx& c, Params& p, long long items) {
+  const int nkb = (p.K + KB - 1) / KB;
+  const int want = static_cast<int>(std::max(1LL, std::min<long long>({8LL, c.num_sms / std::max(1LL, items), nkb / 2})));
+  p.kb_per = (nkb + want - 1) / want;
+  p.split = (nkb + p.kb_per - 1) / p.kb_per;
+}
+
 template <bool DUAL, int NT>
 cudaError_t launch_typed(const Ctx& c, const Fp8GemmArgs& a) {
   CUtensorMap mA, m0, m1;
-  if (!make_maps(a, BOX, &mA, &m0, &m1)) return cudaErrorInvalidValue;
-  const Params p = make_params(c, a, a.b_fmt, a.a_fmt, WM);
-  const long long tiles = a.rows / 16 < a.G ? a.rows : a.rows / 16 + a.G;  // no fewer than there can be
-  const int grid = static_cast<int>(std::max(1LL, std::min<long long>(c.num_sms, tiles * p.n_tiles)));
+  if (!make_maps(a, a.gather ? 1 : BOX, &mA, &m0, &m1)) return cudaErrorInvalidValue;
+  Params p = make_params(c, a, a.b_fmt, a.a_fmt, WM);
+  const long long tiles = a.rows / NT + std::min(a.G, a.rows);  // no fewer than there can be
+  const long long items = tiles * p.n_tiles;
+  if (NT == 32) set_split(c, p, items);
+  p.early = a.early;
   auto kern = fp8_gemm_kernel<DUAL, NT>;
   constexpr size_t smem = kSmem<DUAL, NT>;
   static_assert(smem <= SMEM_MAX && kStages<DUAL, NT> >= 3 && kStages<DUAL, NT> <= 16, "stages");
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(c.num_sms / p.split, items) * p.split));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = c.pdl ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.split > 1 ? 2 : 1;
   KernelScope ks(c, a.name ? a.name : "fp8_gemm");
-  return launch_kernel(c, kern, dim3(grid), dim3(THREADS), smem, mA, m0, m1, p);
+  const cudaError_t le = cudaLaunchKernelEx(&cfg, kern, mA, m0, m1, p);
+  return le != cudaSuccess ? le : cudaGetLastError();
 }
 
+// Mean rows of a group, of the groups that can hold any.
+double mean_rows(int rows, int G) { return static_cast<double>(rows) / std::max(1, std::min(G, rows)); }
+constexpr double kSmallRows = 16.0;
+
 }  // namespace
+
+bool fp8_gemm_gathers(int rows, int G) { return mean_rows(rows, G) <= kSmallRows; }
 
 cudaError_t launch_fp8_gemm(const Ctx& c, const Fp8GemmArgs& a) {
   if (a.rows <= 0 || a.G <= 0) return cudaSuccess;
   if (a.G > MAX_G || a.N % 32 || a.K % 32 || a.N <= 0 || a.K <= 0) return cudaErrorInvalidValue;
-  // Mean rows of a group, of the groups that can hold any.  Measured crossovers with fp8_gemm_rows.cu (64 experts, K and N
-  // of 1024 and 2048): gate/up 62 us here and 71 us there at 48 rows, 76 and 72 us at 64; down 37 and 35 us at 16,
-  // 41 and 35 us at 24.
-  const double rows = static_cast<double>(a.rows) / std::min(a.G, a.rows);
-  if (rows > (a.dual ? 48.0 : 16.0)) return launch_fp8_rows_gemm(c, a);
+  // Measured crossovers with fp8_gemm_rows.cu (64 experts, K and N of 1024 and 2048): gate/up 62 us here and 71 us
+  // there at 48 rows a group, 76 and 72 us at 64; down 37 and 35 us at 16, 41 and 35 us at 24.
+  const double rows = mean_rows(a.rows, a.G);
+  if (a.gather && rows > kSmallRows) return cudaErrorInvalidValue;
+  if (rows > (a.dual ? 48.0 : kSmallRows)) return launch_fp8_rows_gemm(c, a);
   if (!a.dual) return launch_typed<false, 32>(c, a);
-  return rows > 16.0 ? launch_typed<true, 64>(c, a) : launch_typed<true, 32>(c, a);
+  return rows > kSmallRows ? launch_typed<true, 64>(c, a) : launch_typed<true, 32>(c, a);
 }
 
 }  // namespace moe

@@ -23,6 +23,9 @@ struct Params {
   long long a_ld;
   const int32_t* a_scale_map;   // row r uses scale column a_scale_map[r] / a_scale_div
   int a_scale_div;
+  bool gather;                  // row r of A is row a_scale_map[r] / a_scale_div of the tensor (a_ld rows)
+  bool early;                   // weights and offsets were complete before the launch before this one began
+  int split, kb_per;            // CTAs of a cluster that share an item's k-blocks, and k-blocks of each
   const float* s0;
   const float* s1;
   uint32_t idesc;               // without N
@@ -77,6 +80,10 @@ __device__ __forceinline__ void split2(unsigned long long v, float& lo, float& h
   hi = __uint_as_float(b);
 }
 
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a) : "l"(b));
+  return a;
+}
 __device__ __forceinline__ unsigned long long join2(float lo, float hi) {
   return static_cast<unsigned long long>(__float_as_uint(lo)) |
          (static_cast<unsigned long long>(__float_as_uint(hi)) << 32);
@@ -163,7 +170,7 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t groups, uint64_t rows, 
 // Tensor maps of the rows (boxes of a_box) and of one or two weight stacks (boxes of 128 rows).
 bool make_maps(const Fp8GemmArgs& a, uint32_t a_box, CUtensorMap* mA, CUtensorMap* m0, CUtensorMap* m1) {
   const uint64_t G = a.G, N = a.N, K = a.K;
-  return make_map(mA, a.A, 0, static_cast<uint64_t>(a.rows), K, a_box) && make_map(m0, a.B0, G, N, K, WM) &&
+  return make_map(mA, a.A, 0, static_cast<uint64_t>(a.gather ? a.a_ld : a.rows), K, a_box) && make_map(m0, a.B0, G, N, K, WM) &&
          make_map(m1, a.dual ? a.B1 : a.B0, G, N, K, WM);
 }
 
@@ -180,6 +187,9 @@ Params make_params(const Ctx& c, const Fp8GemmArgs& a, int m_fmt, int n_fmt, int
   p.a_ld = a.a_ld;
   p.a_scale_map = a.a_scale_map;
   p.a_scale_div = a.a_scale_div > 0 ? a.a_scale_div : 1;
+  p.gather = a.gather;
+  p.split = 1;
+  p.kb_per = (a.K + KB - 1) / KB;
   p.s0 = a.s0;
   p.s1 = a.s1;
   // kind::f8f6f4 instruction descriptor: D f32, the operands' formats, M

@@ -51,19 +51,17 @@ __device__ __forceinline__ uint2 codes8(const Eight& x, float inv, int fmt) {
 // A CTA codes kTileRows rows x kTileBlocks blocks; a half-warp holds one block (eight values a lane), so the
 // block's maximum is four shuffles.  Scales go through shared memory: the output is [block, row], and a CTA
 // writes runs of kTileRows.  C is a multiple of 32, so eight values are all inside the row or all outside.
+// `sc`: [kTileBlocks][kTileRows + 1] floats of shared memory.
 template <typename XT>
-__global__ void __launch_bounds__(kRowThreads)
-    fp8_rows_kernel(const XT* __restrict__ x, long long stride, int R, int C, int fmt, int pow2,
-                    uint8_t* __restrict__ q, float* __restrict__ scales) {
-  __shared__ float sc[kTileBlocks][kTileRows + 1];
+__device__ __forceinline__ void code_rows(const XT* __restrict__ x, long long stride, int R, int C, int fmt, int pow2,
+                                          uint8_t* __restrict__ q, float* __restrict__ scales, long long row_tile,
+                                          int block_tile, float* sc) {
   const int hw = threadIdx.x >> 4, hl = threadIdx.x & 15;
   const int bl = hw % kTileBlocks;
-  const int kb = blockIdx.y * kTileBlocks + bl;
+  const int kb = block_tile * kTileBlocks + bl;
   const int col = kb * kFp8Block + hl * 8;
   const int left = C - col;
-  const long long row0 = static_cast<long long>(blockIdx.x) * kTileRows;
-  pdl_trigger();
-  pdl_wait();
+  const long long row0 = row_tile * kTileRows;
   constexpr int kPasses = kTileRows / kRowsPerPass, kBatch = 4;
 #pragma unroll 1
   for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
@@ -83,7 +81,7 @@ __global__ void __launch_bounds__(kRowThreads)
       for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
       float scale, inv;
       fp8_scale(m, fmt, pow2 != 0, scale, inv);
-      if (hl == 0) sc[bl][lr] = scale;
+      if (hl == 0) sc[bl * (kTileRows + 1) + lr] = scale;
       if (r < R && left > 0) *reinterpret_cast<uint2*>(q + r * C + col) = codes8(v[u], inv, fmt);
     }
   }
@@ -91,8 +89,87 @@ __global__ void __launch_bounds__(kRowThreads)
   const int nkb = (C + kFp8Block - 1) / kFp8Block;
   for (int i = threadIdx.x; i < kTileBlocks * kTileRows; i += kRowThreads) {
     const int b = i / kTileRows, r = i % kTileRows;
-    if (blockIdx.y * kTileBlocks + b < nkb && row0 + r < R)
-      scales[static_cast<long long>(blockIdx.y * kTileBlocks + b) * R + row0 + r] = sc[b][r];
+    if (block_tile * kTileBlocks + b < nkb && row0 + r < R)
+      scales[static_cast<long long>(block_tile * kTileBlocks + b) * R + row0 + r] = sc[b * (kTileRows + 1) + r];
+  }
+}
+
+template <typename XT>
+__global__ void __launch_bounds__(kRowThreads)
+    fp8_rows_kernel(const XT* __restrict__ x, long long stride, int R, int C, int fmt, int pow2,
+                    uint8_t* __restrict__ q, float* __restrict__ scales) {
+  __shared__ float sc[kTileBlocks * (kTileRows + 1)];
+  pdl_trigger();
+  pdl_wait();
+  code_rows(x, stride, R, C, fmt, pow2, q, scales, blockIdx.x, blockIdx.y, sc);
+}
+
+// Small batches of the 8-bit experts in one launch: CTA 0 sorts the (at most 256) pairs by expert, the others code x.
+// The sort is permute.cu's stable counting sort with one pair a thread: a warp ranks equal experts with
+// __match_any_sync, warps and experts are scanned through shared memory.
+constexpr int kFrontPairs = kRowThreads;
+constexpr int kFrontExperts = 256;
+template <typename XT>
+__global__ void __launch_bounds__(kRowThreads)
+    fp8_front_kernel(const XT* __restrict__ x, int R, int C, uint8_t* __restrict__ q, float* __restrict__ scales,
+                     int row_tiles, const int32_t* __restrict__ ids, int P, int E, int32_t* __restrict__ counts,
+                     int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_pairs,
+                     int32_t* __restrict__ pair_pos, int* status) {
+  __shared__ union {
+    float sc[kTileBlocks * (kTileRows + 1)];
+    int hist[kRowThreads / 32][kFrontExperts];
+  } sm;
+  __shared__ int warp_sum_[kRowThreads / 32];
+  pdl_trigger();
+  if (blockIdx.x > 0) {
+    pdl_wait();
+    const int b = blockIdx.x - 1;
+    code_rows(x, static_cast<long long>(C), R, C, MOE_E4M3, 0, q, scales, b % row_tiles, b / row_tiles, sm.sc);
+    return;
+  }
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+#pragma unroll
+  for (int w = 0; w < kRowThreads / 32; ++w) sm.hist[w][t] = 0;
+  pdl_wait();
+  int e = t < P ? ids[t] : -1;
+  if (t < P && (e < 0 || e >= E)) {
+    record_status(status, MOE_ERR_DEVICE_INDEX);
+    e = -1;
+  }
+  __syncthreads();
+  const unsigned peers = __match_any_sync(0xffffffffu, e);
+  const int rank = __popc(peers & ((1u << lane) - 1u));
+  if (e >= 0 && rank == 0) sm.hist[warp][e] = __popc(peers);
+  __syncthreads();
+  int total = 0;  // thread t: expert t's pairs, and where each warp's begin among them
+#pragma unroll
+  for (int w = 0; w < kRowThreads / 32; ++w) {
+    const int c = sm.hist[w][t];
+    sm.hist[w][t] = total;
+    total += c;
+  }
+  int incl = total;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int n = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += n;
+  }
+  if (lane == 31) warp_sum_[warp] = incl;
+  __syncthreads();
+  int base = incl - total;
+  for (int w = 0; w < warp; ++w) base += warp_sum_[w];
+#pragma unroll
+  for (int w = 0; w < kRowThreads / 32; ++w) sm.hist[w][t] += base;
+  if (t < E) {
+    counts[t] = total;
+    offsets[t] = base;
+    if (t == E - 1) offsets[E] = base + total;
+  }
+  __syncthreads();
+  if (e >= 0) {
+    const int pos = sm.hist[warp][e] + rank;
+    sorted_pairs[pos] = t;
+    pair_pos[t] = pos;
   }
 }
 
@@ -167,11 +244,14 @@ __global__ void __launch_bounds__(256)
       float ww[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const long long p = t * K + k0 + j;
-        const int id = k0 + j < K ? ids[p] : -1;
-        const bool ok = id >= 0 && id < E;
-        ww[j] = ok ? (w ? w[p] : 1.f) : 0.f;
-        v[j] = ok ? load_slot4(y + p * H + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        // the row is loaded beside its id and weight, not after them; one of no expert is memory nobody wrote
+        const long long p = t * K + min(k0 + j, K - 1);
+        const int id = ids[p];
+        const bool ok = k0 + j < K && id >= 0 && id < E;
+        const float wp = w ? w[p] : 1.f;
+        const float4 row = load_slot4(y + p * H + c);
+        ww[j] = ok ? wp : 0.f;
+        v[j] = ok ? row : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -206,6 +286,24 @@ cudaError_t launch_fp8_rows(const Ctx& c, const void* x, int x_dtype, int64_t st
   return launch_kernel(c, fp8_rows_kernel<__nv_bfloat16>, grid, dim3(kRowThreads), 0,
                        static_cast<const __nv_bfloat16*>(x), static_cast<long long>(stride), static_cast<int>(R), C,
                        fmt, pow2 ? 1 : 0, static_cast<uint8_t*>(q), scales);
+}
+
+bool fp8_front_fits(int P, int E) { return P <= kFrontPairs && E <= kFrontExperts; }
+
+cudaError_t launch_fp8_front(const Ctx& c, const void* x, int x_dtype, int R, int C, void* q, float* scales,
+                             const int32_t* ids, int P, int E, int32_t* counts, int32_t* offsets,
+                             int32_t* sorted_pairs, int32_t* pair_pos) {
+  const int nkb = (C + kFp8Block - 1) / kFp8Block;
+  const int row_tiles = (R + kTileRows - 1) / kTileRows;
+  const dim3 grid(1 + row_tiles * ((nkb + kTileBlocks - 1) / kTileBlocks));
+  KernelScope ks(c, "fp8_front");
+  if (x_dtype == MOE_F32)
+    return launch_kernel(c, fp8_front_kernel<float>, grid, dim3(kRowThreads), 0, static_cast<const float*>(x), R, C,
+                         static_cast<uint8_t*>(q), scales, row_tiles, ids, P, E, counts, offsets, sorted_pairs, pair_pos,
+                         c.status);
+  return launch_kernel(c, fp8_front_kernel<__nv_bfloat16>, grid, dim3(kRowThreads), 0,
+                       static_cast<const __nv_bfloat16*>(x), R, C, static_cast<uint8_t*>(q), scales, row_tiles, ids, P,
+                       E, counts, offsets, sorted_pairs, pair_pos, c.status);
 }
 
 cudaError_t launch_fp8_blocks(const Ctx& c, const void* w, int w_dtype, int G, int N, int K, int fmt, bool pow2,

@@ -201,6 +201,11 @@ cudaError_t launch_select_backward(const Ctx& c, const void* logits, int logits_
 // codes [G, N, K] and scales [G, ceil(N/128), ceil(K/128)].
 cudaError_t launch_fp8_rows(const Ctx& c, const void* x, int x_dtype, int64_t stride, int64_t R, int C, int fmt,
                             bool pow2, void* q, float* scales);
+// Coding of dense rows and the permutation of launch_permute in one launch, for small batches.
+bool fp8_front_fits(int P, int E);
+cudaError_t launch_fp8_front(const Ctx& c, const void* x, int x_dtype, int R, int C, void* q, float* scales,
+                             const int32_t* ids, int P, int E, int32_t* counts, int32_t* offsets,
+                             int32_t* sorted_pairs, int32_t* pair_pos);
 cudaError_t launch_fp8_blocks(const Ctx& c, const void* w, int w_dtype, int G, int N, int K, int fmt, bool pow2,
                               void* q, float* scales);
 // out[t] = sum_k w[t,k] y_slots[t*K+k] over the slots with an id in [0, E) (w == nullptr: 1), + y_shared[t].
@@ -218,6 +223,7 @@ struct Fp8GemmArgs {
   int64_t a_ld;
   const int32_t* a_scale_map;
   int a_scale_div;
+  bool gather;           // A too is [a_ld, K], row r its row a_scale_map[r] / a_scale_div (see fp8_gemm_gathers)
   int a_fmt, b_fmt;      // MOE_E4M3 | MOE_E5M2
   int rows, K, N, G;
   const void* B0;
@@ -233,8 +239,13 @@ struct Fp8GemmArgs {
   __nv_bfloat16* out_bf16;
   const int32_t* row_map;
   const float* row_scale;
+  // The launch before this one on the stream is a gate/up product of this file that began after the weights, scales
+  // and offsets here were complete (its kernels wait for their predecessors before they let the next launch start).
+  bool early;
   const char* name;
 };
 cudaError_t launch_fp8_gemm(const Ctx& c, const Fp8GemmArgs& a);
+// Whether a launch of `rows` rows in G groups takes gathered rows (small batches); others want them in group order.
+bool fp8_gemm_gathers(int rows, int G);
 
 }  // namespace moe

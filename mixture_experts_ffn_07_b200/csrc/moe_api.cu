@@ -280,12 +280,16 @@ moe_status fp8_code_x(const moe::Ctx& c, const moe_desc& d, const void* x, void*
 moe_status fp8_experts(const moe::Ctx& c, const moe_desc& d, const moe_weights& w, const int32_t* offsets,
                        const int32_t* sorted_pairs, const float* tw, void* y_slots, void* ws, const Layout& L) {
   const int P = d.T * d.top_k;
-  uint8_t* xp = at<uint8_t>(ws, L.x_perm);
-  // rows of H bytes, moved as rows of H / 2 two-byte elements
-  MOE_TRY(moe::launch_gather_rows(c, at<__nv_bfloat16>(ws, L.x_q), sorted_pairs, offsets, d.E, d.top_k, P, d.H / 2,
-                                  reinterpret_cast<__nv_bfloat16*>(xp)));
   moe::Fp8GemmArgs a{};
-  a.A = xp;
+  a.gather = moe::fp8_gemm_gathers(P, d.E);
+  if (a.gather) {
+    a.A = at<void>(ws, L.x_q);
+  } else {  // rows of H bytes in expert order, moved as rows of H / 2 two-byte elements
+    uint8_t* xp = at<uint8_t>(ws, L.x_perm);
+    MOE_TRY(moe::launch_gather_rows(c, at<__nv_bfloat16>(ws, L.x_q), sorted_pairs, offsets, d.E, d.top_k, P, d.H / 2,
+                                    reinterpret_cast<__nv_bfloat16*>(xp)));
+    a.A = xp;
+  }
   a.a_scale = at<float>(ws, L.x_qs);
   a.a_ld = d.T;
   a.a_scale_map = sorted_pairs;
@@ -324,6 +328,7 @@ moe_status fp8_experts(const moe::Ctx& c, const moe_desc& d, const moe_weights& 
     b.out_f32 = static_cast<float*>(y_slots);
   b.row_map = sorted_pairs;
   b.row_scale = tw;
+  b.early = true;
   b.name = "expert_down_fp8";
   MOE_TRY(moe::launch_fp8_gemm(c, b));
   return MOE_OK;
@@ -364,6 +369,7 @@ moe_status fp8_shared(const moe::Ctx& c, const moe_desc& d, const moe_weights& w
   b.s0 = static_cast<const float*>(w.sh_down_scale);
   b.out_f32 = y_s;
   b.row_scale = gate;
+  b.early = true;
   b.name = "shared_down_fp8";
   MOE_TRY(moe::launch_fp8_gemm(c, b));
   return MOE_OK;
@@ -506,12 +512,19 @@ moe_status experts_impl(const moe::Ctx& c, const moe_desc& d, const void* x, con
   int32_t* sorted_pairs = at<int32_t>(ws, L.sorted_pairs);
   float* y_slots = at<float>(ws, L.y_slots);
   float* y_s = nullptr;
-  moe_status st;
-  MOE_TRY(moe::launch_permute(c, ids, d.T * d.top_k, d.E, at<int32_t>(ws, L.counts), offsets, sorted_pairs,
-                              at<int32_t>(ws, L.pair_pos)));
+  moe_status st = MOE_OK;
   const bool f8 = fp8_path(d), bf16_slots = tensor_path(d);
+  const int P = d.T * d.top_k;
+  const bool front = f8 && moe::fp8_front_fits(P, d.E);
+  if (front)
+    MOE_TRY(moe::launch_fp8_front(c, x, d.act_dtype, d.T, d.H, at<void>(ws, L.x_q), at<float>(ws, L.x_qs), ids, P, d.E,
+                                  at<int32_t>(ws, L.counts), offsets, sorted_pairs, at<int32_t>(ws, L.pair_pos)));
+  else
+    MOE_TRY(moe::launch_permute(c, ids, P, d.E, at<int32_t>(ws, L.counts), offsets, sorted_pairs,
+                                at<int32_t>(ws, L.pair_pos)));
   if (f8) {
-    if ((st = fp8_code_x(c, d, x, ws, L)) != MOE_OK) return st;
+    if (!front) st = fp8_code_x(c, d, x, ws, L);
+    if (st != MOE_OK) return st;
     st = fp8_experts(c, d, w, offsets, sorted_pairs, nullptr, y_slots, ws, L);
   } else {
     st = expert_impl(c, d, x, w, offsets, sorted_pairs, tw, y_slots, ws, L, false, bf16_slots);
