@@ -22,6 +22,8 @@
 // Few items (one decoded token: experts x weight tiles, fewer than SMs) split K over a cluster of up to eight CTAs:
 // each sums its k-blocks, leaves the sums in its shared memory, and the first CTA adds them in rank order.
 // Every wait is bounded; on expiry the CTA records MOE_ERR_TIMEOUT, drains and exits.
+#include <atomic>
+
 #include "fp8_mma.cuh"
 
 namespace moe {
@@ -745,12 +747,43 @@ __global__ void __launch_bounds__(THREADS, 1)
 }
 
 // ------------------------------------------------------------------ host side
-// How many CTAs share an item's k-blocks (1 to 8, of two k-blocks at least each): as many as there are SMs for.
+// Clusters of `size` CTAs of the kernel that fit on the device at once, asked for once per device.
+template <bool DUAL, int NT>
+int resident_clusters(const Ctx& c, int size) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> cached[kMaxDevices][9];  // 1 + the number
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  if (const int v = cached[dev][size].load()) return v - 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(size * (c.num_sms / size));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = kSmem<DUAL, NT>;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = size;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<DUAL, NT>, &cfg) != cudaSuccess) n = 0;
+  cudaGetLastError();
+  cached[dev][size].store(n + 1);
+  return n;
+}
+
+// How many CTAs share an item's k-blocks: as many (up to 8, of two k-blocks at least each) as leave every item's
+// cluster resident at once.  Clusters do not fill the GPU (148 SMs hold 74 of two CTAs, but 45 of three, 15 of eight),
+// and a second wave of them costs more than a wider split gains.
+template <bool DUAL, int NT>
 void set_split(const Ctx& c, Params& p, long long items) {
   const int nkb = (p.K + KB - 1) / KB;
-  const int want = static_cast<int>(std::max(1LL, std::min<long long>({8LL, c.num_sms / std::max(1LL, items), nkb / 2})));
-  p.kb_per = (nkb + want - 1) / want;
-  p.split = (nkb + p.kb_per - 1) / p.kb_per;
+  for (int want = static_cast<int>(std::min<long long>({8LL, c.num_sms / std::max(1LL, items), nkb / 2})); want > 1; --want)
+    if (resident_clusters<DUAL, NT>(c, want) >= items) {
+      p.kb_per = (nkb + want - 1) / want;
+      p.split = (nkb + p.kb_per - 1) / p.kb_per;
+      return;
+    }
 }
 
 template <bool DUAL, int NT>
@@ -760,13 +793,13 @@ cudaError_t launch_typed(const Ctx& c, const Fp8GemmArgs& a) {
   Params p = make_params(c, a, a.b_fmt, a.a_fmt, WM);
   const long long tiles = a.rows / NT + std::min(a.G, a.rows);  // no fewer than there can be
   const long long items = tiles * p.n_tiles;
-  if (NT == 32) set_split(c, p, items);
   p.early = a.early;
   auto kern = fp8_gemm_kernel<DUAL, NT>;
   constexpr size_t smem = kSmem<DUAL, NT>;
   static_assert(smem <= SMEM_MAX && kStages<DUAL, NT> >= 3 && kStages<DUAL, NT> <= 16, "stages");
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
+  if (NT == 32) set_split<DUAL, NT>(c, p, items);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(c.num_sms / p.split, items) * p.split));
   cfg.blockDim = dim3(THREADS);
