@@ -12,44 +12,69 @@ constexpr int kTileRows = 32;    // rows per CTA
 constexpr int kHalfWarps = kRowThreads / 16;
 constexpr int kRowsPerPass = kHalfWarps / kTileBlocks;
 
-struct Eight {
-  float v[8];
+// Eight values as loaded.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  float4 a, b;
 };
-__device__ __forceinline__ Eight load8(const float* p, int left) {
-  Eight r;
-  const float4 a = left > 0 ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
-  const float4 b = left > 4 ? __ldg(reinterpret_cast<const float4*>(p) + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
-  r.v[0] = a.x; r.v[1] = a.y; r.v[2] = a.z; r.v[3] = a.w;
-  r.v[4] = b.x; r.v[5] = b.y; r.v[6] = b.z; r.v[7] = b.w;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 a;
+};
+__device__ __forceinline__ Raw<float> load8(const float* p, int left) {
+  Raw<float> r;
+  r.a = left > 0 ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
+  r.b = left > 4 ? __ldg(reinterpret_cast<const float4*>(p) + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
   return r;
 }
-__device__ __forceinline__ Eight load8(const __nv_bfloat16* p, int left) {
-  Eight r;
-  const uint4 a = left > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+__device__ __forceinline__ Raw<__nv_bfloat16> load8(const __nv_bfloat16* p, int left) {
+  Raw<__nv_bfloat16> r;
+  r.a = left > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+  return r;
+}
+__device__ __forceinline__ void values(const Raw<float>& r, float (&v)[8]) {
+  v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+  v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+}
+__device__ __forceinline__ void values(const Raw<__nv_bfloat16>& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    r.v[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
-    r.v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    v[2 * i] = bf16_bits_to_f32(w[i] & 0xFFFFu);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
-  return r;
 }
-
-__device__ __forceinline__ uint32_t amax_bits(const Eight& x) {
+// Largest |x| as f32 bits (NaN is largest).
+__device__ __forceinline__ uint32_t amax_bits(const Raw<float>& r) {
+  float v[8];
+  values(r, v);
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x.v[i]) & 0x7fffffffu);
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
   return m;
 }
-__device__ __forceinline__ uint2 codes8(const Eight& x, float inv, int fmt) {
+__device__ __forceinline__ uint32_t amax_bits(const Raw<__nv_bfloat16>& r) {
+  // |bf16| patterns order like the numbers: two 16-bit maxima at a time
+  const uint32_t m = __vmaxu2(__vmaxu2(r.a.x & 0x7fff7fffu, r.a.y & 0x7fff7fffu),
+                              __vmaxu2(r.a.z & 0x7fff7fffu, r.a.w & 0x7fff7fffu));
+  return max(m & 0xffff0000u, m << 16);
+}
+template <typename T>
+__device__ __forceinline__ uint2 codes8(const Raw<T>& r, float inv, int fmt) {
+  float v[8];
+  values(r, v);
   uint32_t h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = fp8_pack2(x.v[2 * i] * inv, x.v[2 * i + 1] * inv, fmt);
+  for (int i = 0; i < 4; ++i) h[i] = fp8_pack2(v[2 * i] * inv, v[2 * i + 1] * inv, fmt);
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
-// A CTA codes kTileRows rows x kTileBlocks blocks; a half-warp holds one block (eight values a lane), so the
-// block's maximum is four shuffles.  Scales go through shared memory: the output is [block, row], and a CTA
+// A CTA codes kTileRows rows x kTileBlocks blocks; a half-warp holds one block (eight values a lane) of four rows at a
+// time.  The four maxima are found together (each step over the lanes halves the rows that a lane keeps: five shuffles
+// for four rows), then each quarter of the half-warp makes one row's scale, so the divisions are done once for four
+// rows, and hands its inverse to the others.  Scales go through shared memory: the output is [block, row], and a CTA
 // writes runs of kTileRows.  C is a multiple of 32, so eight values are all inside the row or all outside.
 // `sc`: [kTileBlocks][kTileRows + 1] floats of shared memory.
 template <typename XT>
@@ -66,23 +91,33 @@ __device__ __forceinline__ void code_rows(const XT* __restrict__ x, long long st
 #pragma unroll 1
   for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
     if (row0 + p0 * kRowsPerPass >= R) break;
-    Eight v[kBatch];
+    static_assert(kBatch == 4, "one row per quarter of a half-warp");
+    Raw<XT> v[kBatch];
+    uint32_t m[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
       const long long r = row0 + (p0 + u) * kRowsPerPass + hw / kTileBlocks;
       v[u] = load8(x + (r < R ? r * stride + col : 0), r < R ? left : 0);
     }
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-      const int lr = (p0 + u) * kRowsPerPass + hw / kTileBlocks;
-      const long long r = row0 + lr;
-      uint32_t m = amax_bits(v[u]);
+    for (int u = 0; u < kBatch; ++u) m[u] = amax_bits(v[u]);
+    const bool up8 = hl & 8, up4 = hl & 4;  // lane hl ends with row hl / 4
 #pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      float scale, inv;
-      fp8_scale(m, fmt, pow2 != 0, scale, inv);
-      if (hl == 0) sc[bl * (kTileRows + 1) + lr] = scale;
-      if (r < R && left > 0) *reinterpret_cast<uint2*>(q + r * C + col) = codes8(v[u], inv, fmt);
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t give = up8 ? m[u] : m[u + 2], keep = up8 ? m[u + 2] : m[u];
+      m[u] = max(keep, __shfl_xor_sync(0xffffffffu, give, 8));
+    }
+    uint32_t top = max(up4 ? m[1] : m[0], __shfl_xor_sync(0xffffffffu, up4 ? m[0] : m[1], 4));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    float scale, inv;
+    fp8_scale(top, fmt, pow2 != 0, scale, inv);
+    if ((hl & 3) == 0) sc[bl * (kTileRows + 1) + (p0 + (hl >> 2)) * kRowsPerPass + hw / kTileBlocks] = scale;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const float my_inv = __shfl_sync(0xffffffffu, inv, (threadIdx.x & 16) + 4 * u);
+      const long long r = row0 + (p0 + u) * kRowsPerPass + hw / kTileBlocks;
+      if (r < R && left > 0) *reinterpret_cast<uint2*>(q + r * C + col) = codes8(v[u], my_inv, fmt);
     }
   }
   __syncthreads();
@@ -188,7 +223,7 @@ __global__ void __launch_bounds__(kRowThreads)
   pdl_trigger();
   pdl_wait();
   constexpr int kRows = kFp8Block / kHalfWarps;
-  Eight v[kRows];
+  Raw<XT> v[kRows];
   uint32_t m = 0;
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
