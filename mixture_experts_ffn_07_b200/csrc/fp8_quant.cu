@@ -247,64 +247,105 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-__device__ __forceinline__ float4 load_slot4(const float* p) { return __ldg(reinterpret_cast<const float4*>(p)); }
-__device__ __forceinline__ float4 load_slot4(const __nv_bfloat16* p) {
-  const uint2 a = __ldg(reinterpret_cast<const uint2*>(p));
-  return make_float4(bf16_bits_to_f32(a.x & 0xFFFFu), __uint_as_float(a.x & 0xFFFF0000u),
-                     bf16_bits_to_f32(a.y & 0xFFFFu), __uint_as_float(a.y & 0xFFFF0000u));
+// 16 bytes of a slot row, as floats, and of an output row.
+template <typename T>
+struct Slots;
+template <>
+struct Slots<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void values(const uint4& r, float (&v)[N]) {
+    v[0] = __uint_as_float(r.x); v[1] = __uint_as_float(r.y); v[2] = __uint_as_float(r.z); v[3] = __uint_as_float(r.w);
+  }
+};
+template <>
+struct Slots<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void values(const uint4& r, float (&v)[N]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+};
+template <int N>
+__device__ __forceinline__ void store_row(float* p, const float (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
-__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  *reinterpret_cast<uint2*>(p) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+template <int N>
+__device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&v)[N]) {
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&a);
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; i += 2) *reinterpret_cast<uint2*>(p + 2 * i) = make_uint2(w[i], w[i + 1]);
 }
 
 // out[t] = sum_k w[t,k] y[t*K+k] in slot order in f32 (w == nullptr: 1; slots whose expert id is outside [0, E)
-// hold no row and count nothing), + y_shared[t].  Four outputs a thread.
+// hold no row and count nothing), + y_shared[t].  A CTA has one token and 256 threads' worth of its outputs, 16 bytes
+// of each slot row a thread; the rows are loaded beside the ids and weights, not after them (one of no expert is
+// memory that nobody wrote, and is dropped).
+constexpr int kCombineThreads = 256;
+constexpr int kMaxSlots = 32;
 template <typename T, typename OT>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kCombineThreads)
     combine_ids_kernel(const T* __restrict__ y, const float* __restrict__ w, const int32_t* __restrict__ ids,
-                       const float* __restrict__ y_shared, long long n4, int K, int E, int H4, OT* __restrict__ out) {
+                       const float* __restrict__ y_shared, int K, int E, int H, OT* __restrict__ out) {
+  constexpr int N = Slots<T>::N;
+  __shared__ float weight[kMaxSlots];
+  __shared__ int valid[kMaxSlots];
+  const long long t = blockIdx.x;
+  const int c = (blockIdx.y * kCombineThreads + threadIdx.x) * N;
+  const bool in = c < H;
   pdl_trigger();
   pdl_wait();
-  const long long step = static_cast<long long>(gridDim.x) * blockDim.x;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n4; i += step) {
-    const long long t = i / H4;
-    const int c = static_cast<int>(i - t * H4) * 4;
-    const int H = H4 * 4;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < K; k0 += 8) {
-      float4 v[8];
-      float ww[8];
+  const T* row = y + t * K * H + (in ? c : 0);
+  uint4 r[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        // the row is loaded beside its id and weight, not after them; one of no expert is memory nobody wrote
-        const long long p = t * K + min(k0 + j, K - 1);
-        const int id = ids[p];
-        const bool ok = k0 + j < K && id >= 0 && id < E;
-        const float wp = w ? w[p] : 1.f;
-        const float4 row = load_slot4(y + p * H + c);
-        ww[j] = ok ? wp : 0.f;
-        v[j] = ok ? row : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        acc.x += ww[j] * v[j].x;
-        acc.y += ww[j] * v[j].y;
-        acc.z += ww[j] * v[j].z;
-        acc.w += ww[j] * v[j].w;
-      }
-    }
-    if (y_shared) {
-      const float4 s = __ldg(reinterpret_cast<const float4*>(y_shared + t * H + c));
-      acc.x += s.x;
-      acc.y += s.y;
-      acc.z += s.z;
-      acc.w += s.w;
-    }
-    store4(out + t * H + c, acc);
+  for (int j = 0; j < 8; ++j)
+    if (j < K) r[j] = __ldg(reinterpret_cast<const uint4*>(row + static_cast<long long>(j) * H));
+  if (threadIdx.x < K) {
+    const int id = ids[t * K + threadIdx.x];
+    valid[threadIdx.x] = id >= 0 && id < E;
+    weight[threadIdx.x] = w ? w[t * K + threadIdx.x] : 1.f;
   }
+  float acc[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) acc[i] = 0.f;
+  __syncthreads();
+  if (!in) return;
+  for (int k0 = 0; k0 < K; k0 += 8) {
+    if (k0 > 0)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (k0 + j < K) r[j] = __ldg(reinterpret_cast<const uint4*>(row + static_cast<long long>(k0 + j) * H));
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (k0 + j < K && valid[k0 + j]) {
+        float v[N];
+        Slots<T>::values(r[j], v);
+        const float ww = weight[k0 + j];
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] += ww * v[i];
+      }
+  }
+  if (y_shared) {
+    const float* ys = y_shared + t * H + c;
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(ys + i));
+      acc[i] += v.x;
+      acc[i + 1] += v.y;
+      acc[i + 2] += v.z;
+      acc[i + 3] += v.w;
+    }
+  }
+  store_row<N>(out + t * H + c, acc);
 }
 
 }  // namespace
@@ -355,20 +396,20 @@ cudaError_t launch_fp8_blocks(const Ctx& c, const void* w, int w_dtype, int G, i
 
 template <typename T, typename OT>
 static cudaError_t combine_ids_typed(const Ctx& c, const void* y, const float* w, const int32_t* ids, const float* ys,
-                                     long long n4, int K, int E, int H, void* out) {
-  const unsigned grid = static_cast<unsigned>(std::max(1LL, std::min<long long>((n4 + 255) / 256, 16LL * c.num_sms)));
+                                     int T_, int K, int E, int H, void* out) {
+  const int per = kCombineThreads * Slots<T>::N;
   KernelScope ks(c, "combine");
-  return launch_kernel(c, combine_ids_kernel<T, OT>, dim3(grid), dim3(256), 0, static_cast<const T*>(y), w, ids, ys, n4,
-                       K, E, H / 4, static_cast<OT*>(out));
+  return launch_kernel(c, combine_ids_kernel<T, OT>, dim3(T_, (H + per - 1) / per), dim3(kCombineThreads), 0,
+                       static_cast<const T*>(y), w, ids, ys, K, E, H, static_cast<OT*>(out));
 }
 
 cudaError_t launch_combine_ids(const Ctx& c, const void* y_slots, int y_dtype, const float* w, const int32_t* ids,
                                const float* y_shared, int T, int K, int E, int H, void* out, int dtype) {
-  const long long n4 = static_cast<long long>(T) * (H / 4);
-  if (dtype == MOE_F32) return combine_ids_typed<float, float>(c, y_slots, w, ids, y_shared, n4, K, E, H, out);
+  if (K > kMaxSlots) return cudaErrorInvalidValue;
+  if (dtype == MOE_F32) return combine_ids_typed<float, float>(c, y_slots, w, ids, y_shared, T, K, E, H, out);
   if (y_dtype == MOE_F32)
-    return combine_ids_typed<float, __nv_bfloat16>(c, y_slots, w, ids, y_shared, n4, K, E, H, out);
-  return combine_ids_typed<__nv_bfloat16, __nv_bfloat16>(c, y_slots, w, ids, y_shared, n4, K, E, H, out);
+    return combine_ids_typed<float, __nv_bfloat16>(c, y_slots, w, ids, y_shared, T, K, E, H, out);
+  return combine_ids_typed<__nv_bfloat16, __nv_bfloat16>(c, y_slots, w, ids, y_shared, T, K, E, H, out);
 }
 
 }  // namespace moe
