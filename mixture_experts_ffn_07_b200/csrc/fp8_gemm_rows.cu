@@ -51,23 +51,24 @@ static_assert(SMEM <= SMEM_MAX, "shared memory");
 struct Item {
   int g, wt, row0, n;  // group, weight tile (of 128, or 256 in single mode), first row, rows
 };
+// All lanes of a warp: lane l looks at group 8 l, then lanes 0-7 at the eight groups found (a binary search took a
+// dozen dependent shared loads, about 1000 cycles a tile with the divisions).
 __device__ __forceinline__ Item decode_item(const Aux& aux, int G, int w) {
-  int lo = 0, hi = G - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (aux.item_off[mid] <= w)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
+  const int lane = threadIdx.x & 31;
+  const unsigned coarse = __ballot_sync(0xffffffffu, 8 * lane < G && aux.item_off[min(8 * lane, G)] <= w);
+  const int g0 = 8 * (31 - __clz(coarse));  // item_off[0] == 0: lane 0 always says yes
+  const int mine = min(g0 + (lane & 7), G);
+  const int off = aux.item_off[mine];
+  const unsigned fine = __ballot_sync(0xffffffffu, lane < 8 && mine < G && off <= w);
+  const int k = 31 - __clz(fine);
   Item it;
-  it.g = lo;
-  const int cnt = aux.cnt[lo];
+  it.g = g0 + k;
+  const int local = w - __shfl_sync(0xffffffffu, off, k);
+  const int cnt = aux.cnt[it.g];
   const int tiles = (cnt + TILE_ROWS - 1) / TILE_ROWS;
-  const int local = w - aux.item_off[lo];
-  it.wt = local / tiles;
+  it.wt = tiles == 1 ? local : local / tiles;
   const int tt = local - it.wt * tiles;
-  it.row0 = aux.row_off[lo] + tt * TILE_ROWS;
+  it.row0 = aux.row_off[it.g] + tt * TILE_ROWS;
   it.n = min(TILE_ROWS, cnt - tt * TILE_ROWS);
   return it;
 }
@@ -178,15 +179,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     // 128 x 88 + 256 x 208 = 384 x 168 registers, what the CTA was launched with
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == 0) {
-      if (lane == 0) {
-        // -------------------------------------------------------- TMA producer
-        uint32_t kbg = 0, outstanding = 0, out_phase = 0;
-        bool skipped = false;
-        const uint64_t pol_a = l2_policy_evict_last();    // rows: read by every weight tile
-        const uint64_t pol_w = l2_policy_evict_normal();  // weights: read by every row tile of the group
-        for (int w = blockIdx.x; w < total && !*abort_flag; w += gridDim.x) {
-          const Item it = decode_item(aux, p.G, w);
-          const int n0 = DUAL ? it.wt * WM : 2 * it.wt * WM;
+      // ---------------------------------------------------------- TMA producer (lane 0; the warp finds the items)
+      uint32_t kbg = 0, outstanding = 0, out_phase = 0;
+      bool skipped = false;
+      const uint64_t pol_a = l2_policy_evict_last();    // rows: read by every weight tile
+      const uint64_t pol_w = l2_policy_evict_normal();  // weights: read by every row tile of the group
+      for (int w = blockIdx.x; w < total; w += gridDim.x) {
+        if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
+        const Item it = decode_item(aux, p.G, w);
+        const int n0 = DUAL ? it.wt * WM : 2 * it.wt * WM;
+        if (lane == 0)
           for (int kb = 0; kb < nkb; ++kb, ++kbg) {
             const int s = kbg % STAGES;
             const uint32_t ph = (kbg / STAGES) & 1u;
@@ -205,11 +207,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             outstanding |= 1u << s;
             out_phase = (out_phase & ~(1u << s)) | (ph << s);
           }
-        }
-        if (*abort_flag)  // let issued copies land before the CTA exits
-          for (int s = 0; s < STAGES; ++s)
-            if (outstanding & (1u << s)) wait_cycles(&aux.full[s], (out_phase >> s) & 1u, limit);
+        __syncwarp();
       }
+      if (lane == 0 && *abort_flag)  // let issued copies land before the CTA exits
+        for (int s = 0; s < STAGES; ++s)
+          if (outstanding & (1u << s)) wait_cycles(&aux.full[s], (out_phase >> s) & 1u, limit);
     } else if (warp == 1) {
       if (lane == 0) {
         // -------------------------------------------------------- MMA issuer
@@ -331,18 +333,18 @@ __global__ void __launch_bounds__(THREADS, 1)
           const float2 f = my_sc[(kbg % SLOTS) * TILE_ROWS];  // written before the MMA was issued
           const unsigned long long s0 = DUAL ? join2(f.x, f.x) : (half ? join2(f.y, f.y) : join2(f.x, f.x));
           const unsigned long long s1 = DUAL ? join2(f.y, f.y) : s0;
-          // 16 columns at a time, the next load in flight under the FMAs of the last (loads of 32 need two blocks of 32
-          // consecutive registers beside the 128 accumulators, and spill)
+          // 16 columns at a time and one load in flight: the other warp of the scheduler fills the wait, and no
+          // accumulator spills (two loads of 16 in flight, or one of 32 consecutive registers, spilled a few registers
+          // in this loop and cost a fifth of the time)
           const uint32_t tb = lane_base + buf * ACC;
-          uint32_t v[2][16];
-          tmem_ld_16(tb + load_col(0), v[0]);
 #pragma unroll
           for (int st = 0; st < 8; ++st) {
-            tmem_wait(v[st & 1]);
-            if (st < 7) tmem_ld_16(tb + load_col((st + 1) >> 1) + ((st + 1) & 1) * 16, v[(st + 1) & 1]);
+            uint32_t v[16];
+            tmem_ld_16(tb + load_col(st >> 1) + (st & 1) * 16, v);
+            tmem_wait(v);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              fma2(acc[st >> 1][8 * (st & 1) + i], v[st & 1][2 * i], v[st & 1][2 * i + 1], DUAL && st >= 4 ? s1 : s0);
+              fma2(acc[st >> 1][8 * (st & 1) + i], v[2 * i], v[2 * i + 1], DUAL && st >= 4 ? s1 : s0);
           }
         }
         tc_fence_before();

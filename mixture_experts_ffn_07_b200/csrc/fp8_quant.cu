@@ -76,11 +76,18 @@ __device__ __forceinline__ uint2 codes8(const Raw<T>& r, float inv, int fmt) {
 // for four rows), then each quarter of the half-warp makes one row's scale, so the divisions are done once for four
 // rows, and hands its inverse to the others.  Scales go through shared memory: the output is [block, row], and a CTA
 // writes runs of kTileRows.  C is a multiple of 32, so eight values are all inside the row or all outside.
-// `sc`: [kTileBlocks][kTileRows + 1] floats of shared memory.
+// `sc`: [kTileBlocks][kTileRows + 1] floats of shared memory.  `copies` of each row's codes go out too, where to.pos
+// has a place for them in to.q (none: to.q == nullptr).
+struct Scatter {
+  uint8_t* q;
+  const int32_t* ids;  // [R, K]: a copy exists for ids in [0, E)
+  const int32_t* pos;  // [R, K]: its row
+  int K, E;
+};
 template <typename XT>
 __device__ __forceinline__ void code_rows(const XT* __restrict__ x, long long stride, int R, int C, int fmt, int pow2,
                                           uint8_t* __restrict__ q, float* __restrict__ scales, long long row_tile,
-                                          int block_tile, float* sc) {
+                                          int block_tile, float* sc, const Scatter& to = {}) {
   const int hw = threadIdx.x >> 4, hl = threadIdx.x & 15;
   const int bl = hw % kTileBlocks;
   const int kb = block_tile * kTileBlocks + bl;
@@ -117,7 +124,16 @@ __device__ __forceinline__ void code_rows(const XT* __restrict__ x, long long st
     for (int u = 0; u < kBatch; ++u) {
       const float my_inv = __shfl_sync(0xffffffffu, inv, (threadIdx.x & 16) + 4 * u);
       const long long r = row0 + (p0 + u) * kRowsPerPass + hw / kTileBlocks;
-      if (r < R && left > 0) *reinterpret_cast<uint2*>(q + r * C + col) = codes8(v[u], my_inv, fmt);
+      if (r < R && left > 0) {
+        const uint2 code = codes8(v[u], my_inv, fmt);
+        if (q) *reinterpret_cast<uint2*>(q + r * C + col) = code;
+        if (to.q)
+          for (int k = 0; k < to.K; ++k) {
+            const int id = to.ids[r * to.K + k];
+            if (id >= 0 && id < to.E)
+              *reinterpret_cast<uint2*>(to.q + static_cast<long long>(to.pos[r * to.K + k]) * C + col) = code;
+          }
+      }
     }
   }
   __syncthreads();
@@ -137,6 +153,18 @@ __global__ void __launch_bounds__(kRowThreads)
   pdl_trigger();
   pdl_wait();
   code_rows(x, stride, R, C, fmt, pow2, q, scales, blockIdx.x, blockIdx.y, sc);
+}
+
+// The activations of a large batch in expert order: x is read once, and each token's codes written to the rows of its
+// pairs (coding first and copying rows after read them back K times: 181 us for 8192 tokens of 7168, 8 experts each).
+template <typename XT>
+__global__ void __launch_bounds__(kRowThreads)
+    fp8_scatter_kernel(const XT* __restrict__ x, int R, int C, uint8_t* __restrict__ q, float* __restrict__ scales,
+                       const Scatter to) {
+  __shared__ float sc[kTileBlocks * (kTileRows + 1)];
+  pdl_trigger();
+  pdl_wait();
+  code_rows(x, static_cast<long long>(C), R, C, MOE_E4M3, 0, q, scales, blockIdx.x, blockIdx.y, sc, to);
 }
 
 // Small batches of the 8-bit experts in one launch: CTA 0 sorts the (at most 256) pairs by expert, the others code x.
@@ -362,6 +390,19 @@ cudaError_t launch_fp8_rows(const Ctx& c, const void* x, int x_dtype, int64_t st
   return launch_kernel(c, fp8_rows_kernel<__nv_bfloat16>, grid, dim3(kRowThreads), 0,
                        static_cast<const __nv_bfloat16*>(x), static_cast<long long>(stride), static_cast<int>(R), C,
                        fmt, pow2 ? 1 : 0, static_cast<uint8_t*>(q), scales);
+}
+
+cudaError_t launch_fp8_scatter(const Ctx& c, const void* x, int x_dtype, int R, int C, void* q, float* scales,
+                               const int32_t* ids, const int32_t* pair_pos, int K, int E, void* x_perm) {
+  const int nkb = (C + kFp8Block - 1) / kFp8Block;
+  const dim3 grid((R + kTileRows - 1) / kTileRows, (nkb + kTileBlocks - 1) / kTileBlocks);
+  const Scatter to{static_cast<uint8_t*>(x_perm), ids, pair_pos, K, E};
+  KernelScope ks(c, "fp8_scatter");
+  if (x_dtype == MOE_F32)
+    return launch_kernel(c, fp8_scatter_kernel<float>, grid, dim3(kRowThreads), 0, static_cast<const float*>(x), R, C,
+                         static_cast<uint8_t*>(q), scales, to);
+  return launch_kernel(c, fp8_scatter_kernel<__nv_bfloat16>, grid, dim3(kRowThreads), 0,
+                       static_cast<const __nv_bfloat16*>(x), R, C, static_cast<uint8_t*>(q), scales, to);
 }
 
 bool fp8_front_fits(int P, int E) { return P <= kFrontPairs && E <= kFrontExperts; }

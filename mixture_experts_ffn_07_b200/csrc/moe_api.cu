@@ -275,19 +275,21 @@ moe_status fp8_code_x(const moe::Ctx& c, const moe_desc& d, const void* x, void*
   return MOE_OK;
 }
 
-// Routed experts on 8-bit floats; x is coded already.  tw: slot rows in f32 times the routing weight
+// Routed experts on 8-bit floats; x is coded already (in_order: in the workspace's x_perm, in expert order).  tw: slot rows in f32 times the routing weight
 // (moe_expert_ffn); without it slot rows in act_dtype for launch_combine_ids.
 moe_status fp8_experts(const moe::Ctx& c, const moe_desc& d, const moe_weights& w, const int32_t* offsets,
-                       const int32_t* sorted_pairs, const float* tw, void* y_slots, void* ws, const Layout& L) {
+                       const int32_t* sorted_pairs, const float* tw, void* y_slots, void* ws, const Layout& L,
+                       bool in_order = false) {
   const int P = d.T * d.top_k;
   moe::Fp8GemmArgs a{};
   a.gather = moe::fp8_gemm_gathers(P, d.E);
   if (a.gather) {
     a.A = at<void>(ws, L.x_q);
-  } else {  // rows of H bytes in expert order, moved as rows of H / 2 two-byte elements
+  } else {  // rows in expert order: there already, or copied (rows of H bytes as rows of H / 2 two-byte elements)
     uint8_t* xp = at<uint8_t>(ws, L.x_perm);
-    MOE_TRY(moe::launch_gather_rows(c, at<__nv_bfloat16>(ws, L.x_q), sorted_pairs, offsets, d.E, d.top_k, P, d.H / 2,
-                                    reinterpret_cast<__nv_bfloat16*>(xp)));
+    if (!in_order)
+      MOE_TRY(moe::launch_gather_rows(c, at<__nv_bfloat16>(ws, L.x_q), sorted_pairs, offsets, d.E, d.top_k, P, d.H / 2,
+                                      reinterpret_cast<__nv_bfloat16*>(xp)));
     a.A = xp;
   }
   a.a_scale = at<float>(ws, L.x_qs);
@@ -523,9 +525,15 @@ moe_status experts_impl(const moe::Ctx& c, const moe_desc& d, const void* x, con
     MOE_TRY(moe::launch_permute(c, ids, P, d.E, at<int32_t>(ws, L.counts), offsets, sorted_pairs,
                                 at<int32_t>(ws, L.pair_pos)));
   if (f8) {
-    if (!front) st = fp8_code_x(c, d, x, ws, L);
+    const bool scatter = !front && !moe::fp8_gemm_gathers(P, d.E);
+    if (scatter)
+      MOE_TRY(moe::launch_fp8_scatter(c, x, d.act_dtype, d.T, d.H, d.shared_I > 0 ? at<void>(ws, L.x_q) : nullptr,
+                                      at<float>(ws, L.x_qs), ids, at<int32_t>(ws, L.pair_pos), d.top_k, d.E,
+                                      at<void>(ws, L.x_perm)));
+    else if (!front)
+      st = fp8_code_x(c, d, x, ws, L);
     if (st != MOE_OK) return st;
-    st = fp8_experts(c, d, w, offsets, sorted_pairs, nullptr, y_slots, ws, L);
+    st = fp8_experts(c, d, w, offsets, sorted_pairs, nullptr, y_slots, ws, L, scatter);
   } else {
     st = expert_impl(c, d, x, w, offsets, sorted_pairs, tw, y_slots, ws, L, false, bf16_slots);
   }

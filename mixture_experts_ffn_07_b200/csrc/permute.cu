@@ -134,13 +134,14 @@ __global__ void __launch_bounds__(kWarps * 32) permute_kernel(const int32_t* __r
 }
 
 // The same stable counting sort for up to 8 x 8192 pairs, by a cluster of up to
-// 8 CTAs.  CTA b owns pairs [8192 b, 8192 (b+1)), each thread 8 of them held in
-// registers (warp w: 256 consecutive pairs in 8 rounds of 32).  CTA-level
+// 8 CTAs.  CTA b owns the b-th chunk of 1024 x kPerThread pairs (kPerThread 1 to
+// 8: the fewest rounds that eight CTAs need), each thread kPerThread of them held
+// in registers (warp w: consecutive pairs in rounds of 32).  CTA-level
 // expert counts are exchanged through distributed shared memory, so the pairs
 // are read from memory once and no global scratch is needed.
-constexpr int kPerThread = 8;
-constexpr int kClusterChunk = kWarps * 32 * kPerThread;  // 8192 pairs per CTA
+constexpr int kMaxPerThread = 8;
 
+template <int kPerThread>
 __global__ void __launch_bounds__(kWarps * 32) permute_cluster_kernel(const int32_t* __restrict__ ids, int P, int E,
                                                                        int32_t* __restrict__ counts,
                                                                        int32_t* __restrict__ offsets,
@@ -157,7 +158,7 @@ __global__ void __launch_bounds__(kWarps * 32) permute_cluster_kernel(const int3
   pdl_trigger();
   for (int i = threadIdx.x; i < kWarps * kMaxE; i += blockDim.x) (&hist[0][0])[i] = 0;
   pdl_wait();
-  const int base = rank * kClusterChunk + warp * 32 * kPerThread;
+  const int base = (rank * kWarps + warp) * 32 * kPerThread;
   int e[kPerThread];
 #pragma unroll
   for (int j = 0; j < kPerThread; ++j) {
@@ -280,28 +281,41 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const uint4* __restric
 
 }  // namespace
 
+namespace {
+
+template <int kPerThread>
+cudaError_t launch_permute_cluster(const Ctx& c, const int32_t* ids, int P, int E, int32_t* counts, int32_t* offsets,
+                                   int32_t* sorted_pairs, int32_t* pair_pos) {
+  constexpr int chunk = kWarps * 32 * kPerThread;
+  const int ncta = std::max(1, (P + chunk - 1) / chunk);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ncta);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = c.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = c.pdl ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ncta;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  KernelScope ks(c, "permute");
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, permute_cluster_kernel<kPerThread>, ids, P, E, counts, offsets,
+                                           sorted_pairs, pair_pos, c.status);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_permute(const Ctx& c, const int32_t* ids, int P, int E, int32_t* counts, int32_t* offsets,
                            int32_t* sorted_pairs, int32_t* pair_pos) {
-  if (P <= kCluster * kClusterChunk) {
-    const int ncta = std::max(1, (P + kClusterChunk - 1) / kClusterChunk);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ncta);
-    cfg.blockDim = dim3(kWarps * 32);
-    cfg.stream = c.stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = c.pdl ? 1 : 0;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ncta;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    KernelScope ks(c, "permute");
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, permute_cluster_kernel, ids, P, E, counts, offsets, sorted_pairs,
-                                             pair_pos, c.status);
-    return e != cudaSuccess ? e : cudaGetLastError();
-  }
+  constexpr int per = kCluster * kWarps * 32;  // pairs of one round of eight CTAs
+  if (P <= per) return launch_permute_cluster<1>(c, ids, P, E, counts, offsets, sorted_pairs, pair_pos);
+  if (P <= 2 * per) return launch_permute_cluster<2>(c, ids, P, E, counts, offsets, sorted_pairs, pair_pos);
+  if (P <= 4 * per) return launch_permute_cluster<4>(c, ids, P, E, counts, offsets, sorted_pairs, pair_pos);
+  if (P <= kMaxPerThread * per) return launch_permute_cluster<8>(c, ids, P, E, counts, offsets, sorted_pairs, pair_pos);
   KernelScope ks(c, "permute");
   return launch_kernel(c, permute_kernel, dim3(1), dim3(kWarps * 32), 0, ids, P, E, counts, offsets, sorted_pairs,
                        pair_pos, c.status);
