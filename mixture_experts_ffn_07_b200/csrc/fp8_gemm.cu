@@ -15,9 +15,13 @@
 // k-block out of TMEM and add it, scaled, to f32 registers while the next ones run.
 //  * warp 0: TMA producer (weight tiles 128 x 128 bytes; token rows in boxes of 32, 128-byte swizzle, or, for the
 //    routed gate/up of small batches, gathered row by row straight from the tokens with tile::gather4);
-//  * warp 1: allocates TMEM, issues tcgen05.mma kind::f8f6f4 from one lane;
-//  * warps 2 and 3: load the scales of each k-block, multiply row and tile scale, into a ring;
-//  * warps 4-11: epilogue; warp w reads TMEM lanes 32 (w % 4) and one half of the columns.
+//  * warp 1: allocates TMEM, issues tcgen05.mma kind::f8f6f4 from one lane; with tiles of 32 rows warp 3 issues every
+//    second k-block: each has an accumulator of its own, and a k-block costs its issuer two barrier waits, four
+//    instructions and a commit, 600-800 cycles, more than its copies take;
+//  * warp 2 (and 3 with tiles of 64): loads the scales of each k-block, multiplies row and tile scale, into a ring;
+//  * warps 4-11: epilogue; warp w reads TMEM lanes 32 (w % 4), and one half of the columns, or, with at most 16 rows,
+//    every second k-block.
+// A k-block's stage and accumulator have the same number, and one commit frees the stage and fills the accumulator.
 //
 // Few items (one decoded token: experts x weight tiles, fewer than SMs) split K over a cluster of up to eight CTAs:
 // each sums its k-blocks, leaves the sums in its shared memory, and the first CTA adds them in rank order.
@@ -39,16 +43,23 @@ struct Cfg {
   static constexpr int MATS = DUAL ? 2 : 1;
   static constexpr int STAGE_BYTES = MATS * W_BYTES + NT * KB;
   static constexpr int ACC = MATS * NT;                      // TMEM columns of one accumulator
-  static constexpr int NBUF = 512 / ACC < 8 ? 512 / ACC : 8; // accumulators
-  static constexpr uint32_t TMEM_COLS = NBUF * ACC;
+  // Stages, and accumulators.  An even number: a k-block's stage then always belongs to the same MMA warp and, with at
+  // most 16 rows, to the same half of the epilogue, so each of them sees every phase of the barriers that it waits for
+  // (waiting for a phase by its parity while the one before is still open would pass at once).
+  static constexpr int RING = NT == 32 && !DUAL ? 8 : 4;
+  static_assert(RING % 2 == 0, "phases");
+  static constexpr uint32_t TMEM_COLS = RING * ACC <= 256 ? 256 : 512;
+  static_assert(RING * ACC <= 512 && NT <= 64, "TMEM columns");
   static constexpr int HALF = NT / 2;                        // columns per epilogue warp
   static constexpr int X = HALF / 8 < 8 ? HALF / 8 : 8;      // 8-column groups per TMEM load
   static constexpr int CHUNKS = HALF / (8 * X);
   static constexpr int SCALE_WARPS = NT > 32 ? 2 : 1;
-  // Ring of scales.  The scale warps write a k-block's slot after its stage came free, that is after the MMA STAGES
-  // k-blocks earlier, which the epilogue's reads of the k-block NBUF before that one (values and scales) precede: a
-  // slot STAGES + NBUF k-blocks old is read, and the ring needs no barriers of its own.
-  static constexpr int SLOTS = NT == 32 ? 32 : 16;
+  static constexpr int MMA_WARPS = NT > 32 ? 1 : 2;
+  // Ring of scales.  The scale warps write a k-block's slot after its stage came free, that is after the MMA RING
+  // k-blocks earlier, which the epilogue's reads of the k-block RING before that one (values and scales) precede: a
+  // slot 2 RING k-blocks old is read, and the ring needs no barriers of its own.
+  static constexpr int SLOTS = 16;
+  static_assert(SLOTS >= 2 * RING, "ring of scales");
   static constexpr int OUT_STAGE = DUAL ? NT * PITCH8 : EPI_WARPS * 16 * PITCH16;
 };
 
@@ -57,18 +68,19 @@ struct Item {
   bool alone;          // the group has one token tile: its weights are read once
 };
 
-template <bool DUAL, int NT, int STAGES>
+template <bool DUAL, int NT>
 struct Aux {
   alignas(16) float sc[Cfg<DUAL, NT>::SLOTS][DUAL ? 2 : 1][NT];  // row scale x tile scale
   alignas(16) float inv[DUAL ? NT : 4];           // dual: 1 / h scale of each column
   uint32_t red[DUAL ? EPI_WARPS : 1][NT / 2];     // dual: largest |h| of each warp's columns, as bits
   int dest[2][DUAL ? 4 : NT];                     // single: output row of each column (-1: none)
   float rscale[2][DUAL ? 4 : NT];
-  uint64_t full[STAGES];
-  uint64_t empty[STAGES];
-  uint64_t tfull[8];
-  uint64_t tempty[8];
-  uint64_t done;
+  // tiles of 32 rows, at most 16 of them in use: the sums of the epilogue's second half
+  unsigned long long alt[NT == 32 ? Cfg<DUAL, NT>::MATS * 8 : 1][EPI_WARPS * 16];
+  uint64_t full[Cfg<DUAL, NT>::RING];
+  uint64_t done[Cfg<DUAL, NT>::RING];    // the k-block's MMAs: its stage is free and its accumulator full
+  uint64_t tempty[Cfg<DUAL, NT>::RING];
+  uint64_t all_done;
   uint32_t tmem_base;
   int abort;
   int item_off[MAX_G + 1];
@@ -77,13 +89,9 @@ struct Aux {
   Item first;  // this CTA's first item
 };
 
-// As many stages as fit beside the rest.
 template <bool DUAL, int NT>
-constexpr int kStages = (SMEM_MAX - 1024 - static_cast<int>(sizeof(Aux<DUAL, NT, 16>)) - Cfg<DUAL, NT>::OUT_STAGE) /
-                        Cfg<DUAL, NT>::STAGE_BYTES;
-template <bool DUAL, int NT>
-constexpr size_t kSmem = 1024 + static_cast<size_t>(kStages<DUAL, NT>) * Cfg<DUAL, NT>::STAGE_BYTES +
-                         Cfg<DUAL, NT>::OUT_STAGE + sizeof(Aux<DUAL, NT, kStages<DUAL, NT>>);
+constexpr size_t kSmem = 1024 + static_cast<size_t>(Cfg<DUAL, NT>::RING) * Cfg<DUAL, NT>::STAGE_BYTES +
+                         Cfg<DUAL, NT>::OUT_STAGE + sizeof(Aux<DUAL, NT>);
 
 // 16 TMEM lanes x 8 X columns.  Group i of 8 columns: registers 4 i, 4 i + 1 hold columns 2 (lane % 4), + 1 of row
 // lane / 4, registers 4 i + 2, 4 i + 3 the same columns of row lane / 4 + 8.  So a thread needs two of the eight
@@ -186,14 +194,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapW0,
                     const __grid_constant__ CUtensorMap mapW1, const Params p) {
   using C = Cfg<DUAL, NT>;
-  constexpr int STAGES = kStages<DUAL, NT>;
-  constexpr int NBUF = C::NBUF;
+  constexpr int RING = C::RING;
   constexpr int SLOTS = C::SLOTS;
-  static_assert(SLOTS >= STAGES + NBUF, "ring of scales");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* out_stage = smem + STAGES * C::STAGE_BYTES;
-  Aux<DUAL, NT, STAGES>& aux = *reinterpret_cast<Aux<DUAL, NT, STAGES>*>(out_stage + C::OUT_STAGE);
+  uint8_t* out_stage = smem + RING * C::STAGE_BYTES;
+  Aux<DUAL, NT>& aux = *reinterpret_cast<Aux<DUAL, NT>*>(out_stage + C::OUT_STAGE);
   volatile int* abort_flag = &aux.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool split = p.split > 1;
@@ -201,15 +207,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int first = split ? cluster_id() : blockIdx.x, step = split ? clusters() : gridDim.x;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < RING; ++s) {
       mbar_init(&aux.full[s], 1 + C::SCALE_WARPS);
-      mbar_init(&aux.empty[s], 1);
+      mbar_init(&aux.done[s], 1);
+      mbar_init(&aux.tempty[s], EPI_WARPS);
     }
-    for (int b = 0; b < NBUF; ++b) {
-      mbar_init(&aux.tfull[b], 1);
-      mbar_init(&aux.tempty[b], EPI_WARPS);
-    }
-    mbar_init(&aux.done, 1);
+    mbar_init(&aux.all_done, C::MMA_WARPS);
     aux.abort = 0;
     fence_mbar_init();
   } else if (threadIdx.x == 64) {
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           // The first item's first stages are free, and a lane fills each: waiting for and arriving on a barrier takes
           // a lane a few hundred cycles, which one lane would spend stage after stage.  Weights before rows, whose
           // indexes (gathered) or values (early) are still on their way.
-          const int fill = min(STAGES, kb_hi - kb_lo);
+          const int fill = min(RING, kb_hi - kb_lo);
           const bool mine = lane < fill && !(p.skip_stage && lane == 0 && blockIdx.x == 0);  // debug: one stage unfilled
           uint8_t* st = smem + lane * C::STAGE_BYTES;
           const int x = (kb_lo + lane) * KB;
@@ -333,10 +336,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int n = done; n < kb_hi - kb_lo; ++n) {
           const int kb = kb_lo + n;
           const uint32_t k = kbg + n;
-          const int s = k % STAGES;
-          const uint32_t ph = (k / STAGES) & 1u;
+          const int s = k % RING;
+          const uint32_t ph = (k / RING) & 1u;
           int got = 1;
-          if (lane == 0) got = mbar_wait_bounded(&aux.empty[s], ph ^ 1u, limit, abort_flag);
+          if (lane == 0) got = mbar_wait_bounded(&aux.done[s], ph ^ 1u, limit, abort_flag);
           if (!__shfl_sync(0xffffffffu, got, 0)) break;
           outstanding &= ~(1u << s);
           uint8_t* st = smem + s * C::STAGE_BYTES;
@@ -361,10 +364,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       pass_item(split);
     }
     if (lane == 0 && *abort_flag)  // let issued copies land before the CTA exits
-      for (int s = 0; s < STAGES; ++s)
+      for (int s = 0; s < RING; ++s)
         if (outstanding & (1u << s)) wait_cycles(&aux.full[s], (out_phase >> s) & 1u, limit);
-  } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer (one lane)
+  } else if (warp == 1 || (warp == 3 && C::MMA_WARPS == 2)) {
+    // ---------------------------------------------------------- MMA issuers (one lane; k-blocks in turn)
+    const uint32_t mine = warp >> 1;
     uint32_t kbg = 0;
     bool ok = true;
     for (int w = first; w < total; w += step) {
@@ -373,10 +377,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t n16 = (it.n + 15) & ~15;
         const uint32_t idesc = p.idesc | ((n16 >> 3) << 17);
         for (int kb = kb_lo; kb < kb_hi; ++kb, ++kbg) {
-          const int s = kbg % STAGES;
-          const int buf = kbg % NBUF;
-          if (!mbar_wait_bounded(&aux.tempty[buf], ((kbg / NBUF) & 1u) ^ 1u, limit, abort_flag) ||
-              !mbar_wait_bounded(&aux.full[s], (kbg / STAGES) & 1u, limit, abort_flag)) {
+          if (C::MMA_WARPS == 2 && (kbg & 1u) != mine) continue;
+          const int s = kbg % RING;
+          const uint32_t round = kbg / RING;
+          if ((round > 0 && !mbar_wait_bounded(&aux.tempty[s], (round & 1u) ^ 1u, limit, abort_flag)) ||
+              !mbar_wait_bounded(&aux.full[s], round & 1u, limit, abort_flag)) {
             ok = false;
             break;
           }
@@ -386,21 +391,20 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int m = 0; m < C::MATS; ++m) {
             const uint64_t wdesc = sw128_kmajor_desc(st + m * W_BYTES);
-            const uint32_t d = tmem_base + buf * C::ACC + m * NT;
+            const uint32_t d = tmem_base + s * C::ACC + m * NT;
 #pragma unroll
             for (int kk = 0; kk < KB / 32; ++kk)
               umma_f8(d, wdesc + static_cast<uint64_t>(kk * 2), tdesc + static_cast<uint64_t>(kk * 2), idesc,
                       kk > 0 ? 1u : 0u);
           }
-          umma_commit(&aux.empty[s]);
-          umma_commit(&aux.tfull[buf]);
+          umma_commit(&aux.done[s]);
         }
       }
       pass_item(split);
     }
     if (lane == 0) {
-      umma_commit(&aux.done);  // every MMA issued above completes before TMEM is released
-      wait_cycles(&aux.done, 0, limit);
+      umma_commit(&aux.all_done);  // every MMA issued completes before TMEM is released
+      wait_cycles(&aux.all_done, 0, limit);
     }
   } else if (warp < 4) {
     // ---------------------------------------------------------- scales: warp 2 + i has the i-th part of the columns.
@@ -435,8 +439,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int b = 0; b < AHEAD; ++b) {  // unrolled, so that a scale in flight is never moved between registers
             if (kb0 + b >= kb_hi) break;
-            const int s = kbg % STAGES;
-            const bool got = mbar_wait_bounded(&aux.empty[s], ((kbg / STAGES) & 1u) ^ 1u, limit, abort_flag);
+            const int s = kbg % RING;
+            const bool got = mbar_wait_bounded(&aux.done[s], ((kbg / RING) & 1u) ^ 1u, limit, abort_flag);
             if (!__all_sync(0xffffffffu, got)) {
               ok = false;
               break;
@@ -473,6 +477,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Item it = w == first ? aux.first : decode_item<NT>(aux, p.G, w);
       const int wt = it.wt;
       const int n16 = (it.n + 15) & ~15;
+      const bool alt = NT == 32 && it.n <= 16;  // the halves take k-blocks in turn, both the first 16 columns
+      const int col0 = alt ? 0 : half * HALF;
       if (!DUAL) {  // output row and scale of each column
         for (int c = et; c < NT; c += EPI_WARPS * 32) {
           int d = -1;
@@ -500,14 +506,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           for (int j = 0; j < 2 * X; ++j) acc[m][c][0][j] = acc[m][c][1][j] = 0ull;
       bool ok = alive;
       for (int kb = kb_lo; kb < kb_hi && ok; ++kb, ++kbg) {
-        const int slot = kbg % SLOTS, buf = kbg % NBUF;
-        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&aux.tfull[buf], (kbg / NBUF) & 1u, limit, abort_flag))) {
+        // (the barrier after the item's last k-block closes the phases that the other half has waited for)
+        if (alt && (kbg & 1u) != half) continue;
+        const int slot = kbg % SLOTS, buf = kbg % RING;
+        if (!__all_sync(0xffffffffu, mbar_wait_bounded(&aux.done[buf], (kbg / RING) & 1u, limit, abort_flag))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (half * HALF < n16) {  // warp-uniform
-          const uint32_t tb = tmem_base + lane_base + buf * C::ACC + half * HALF;
+        if (col0 < n16) {  // warp-uniform
+          const uint32_t tb = tmem_base + lane_base + buf * C::ACC + col0;
           unsigned long long sc[X];
 #pragma unroll
           for (int st = 0; st < STEPS; ++st) {
@@ -517,7 +525,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (r == 0) {
 #pragma unroll
               for (int i = 0; i < X; ++i)
-                sc[i] = *reinterpret_cast<const unsigned long long*>(&aux.sc[slot][m][half * HALF + 8 * (c * X + i) + lc]);
+                sc[i] = *reinterpret_cast<const unsigned long long*>(&aux.sc[slot][m][col0 + 8 * (c * X + i) + lc]);
             }
             tmem_wait(v);
 #pragma unroll
@@ -529,17 +537,31 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&aux.tempty[buf]);
+        if (lane == 0) {
+          mbar_arrive(&aux.tempty[buf]);
+          if (alt) mbar_arrive(&aux.tempty[buf]);  // for the other half's warp
+        }
       }
       // uniform over the epilogue: either every warp has all k-blocks or the tile is dropped; also orders dest
       alive = named_barrier_and(1, EPI_WARPS * 32, ok);
+      if (alt) {
+        constexpr int VALS = MATS * CHUNKS * 4 * X;
+        unsigned long long* flat = &acc[0][0][0][0];
+        unsigned long long* at = &aux.alt[0][et & 127];
+        if (half)
+#pragma unroll
+          for (int j = 0; j < VALS; ++j) at[j * 128] = flat[j];
+        named_barrier(1, EPI_WARPS * 32);
+#pragma unroll
+        for (int j = 0; j < VALS; ++j) flat[j] = half ? 0ull : add2(flat[j], at[j * 128]);
+      }
       if (split) {
         // The k-ranges' sums, left in each CTA's first stages (every copy into them has been used) and added in rank
         // order.  Distributed shared memory passes about 20 bytes a cycle, so only columns in use are read; a plain
         // product is added and written by all the CTAs, each a part of the values, h by the first one, which needs
         // whole columns for their scales.
         constexpr int VALS = MATS * CHUNKS * 4 * X, PITCH = EPI_WARPS * 32;
-        static_assert(VALS * PITCH * 8 <= STAGES * C::STAGE_BYTES, "partial sums");
+        static_assert(VALS * PITCH * 8 <= RING * C::STAGE_BYTES, "partial sums");
         unsigned long long* mine = reinterpret_cast<unsigned long long*>(smem) + et;
         unsigned long long* flat = &acc[0][0][0][0];  // value j: columns 8 ((j / 2) % X) + lc, + 1 of a row
 #pragma unroll
@@ -796,7 +818,7 @@ cudaError_t launch_typed(const Ctx& c, const Fp8GemmArgs& a) {
   p.early = a.early;
   auto kern = fp8_gemm_kernel<DUAL, NT>;
   constexpr size_t smem = kSmem<DUAL, NT>;
-  static_assert(smem <= SMEM_MAX && kStages<DUAL, NT> >= 3 && kStages<DUAL, NT> <= 16, "stages");
+  static_assert(smem <= SMEM_MAX, "shared memory");
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   if (NT == 32) set_split<DUAL, NT>(c, p, items);

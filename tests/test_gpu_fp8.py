@@ -529,3 +529,140 @@ def test_deterministic():
         one = _experts(d1, x[i:i + 1].contiguous(), t, ids[i:i + 1].contiguous(), tw[i:i + 1].contiguous())
         want, tol = _expected(x[i:i + 1], ids[i:i + 1], tw[i:i + 1], None, t, E, "silu")
         assert torch.all((one.double() - want).abs() <= tol)
+
+
+@pytest.mark.parametrize("M,N,K", [(2, 64, 4128), (16, 352, 7200), (5, 32, 2048), (31, 96, 4992), (32, 32, 8192)])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_product_few_items_split_over_k(M, N, K, out):
+    """Few tiles: the k-blocks are shared by CTAs of a cluster, in parts that do not divide evenly."""
+    a, sa, b, sb = _operands(M, 1, N, K, "e4m3", "e4m3", M + N + K)
+    first = _product(a, sa, b, sb, None, out)
+    _check_product(first, a, sa, b, sb, [0, M])
+    for _ in range(20):
+        assert torch.equal(_product(a, sa, b, sb, None, out), first)
+
+
+@pytest.mark.parametrize("M,off", [(300, None), (300, [0, 130, 131, 290]), (20, [0, 3, 9, 20])])
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16])
+def test_product_output_at_sixteen_bytes(M, off, out):
+    """Outputs on a 16-byte boundary that is no 32-byte one, inside a larger buffer whose rest is left alone."""
+    G = 1 if off is None else 3
+    a, sa, b, sb = _operands(M, G, 160, 416, "e4m3", "e4m3", 9)
+    pad = 16 // out.itemsize
+    buf = torch.full((M * 160 + 2 * pad,), float("nan"), dtype=out, device="cuda")
+    assert buf.data_ptr() % 32 == 0
+    y = buf[pad:-pad].view(M, 160)
+    off_d = None if off is None else torch.tensor(off, dtype=torch.int32, device="cuda")
+    moe.fp8_gemm(a, sa, b, sb, y, offsets=off_d)
+    _ok()
+    _check_product(y, a, sa, b, sb, off or [0, M])
+    assert torch.isnan(buf[:pad].float()).all() and torch.isnan(buf[-pad:].float()).all()
+
+
+def _spread_routing(T, E, K, seed):
+    """Ids whose experts hold from none to many rows."""
+    g = _gen(seed)
+    lean = torch.exp(2 * torch.randn(E, generator=g, device="cuda"))
+    return torch.multinomial(lean.expand(T, E), K, generator=g).to(torch.int32), torch.rand((T, K), generator=g, device="cuda")
+
+
+@pytest.mark.parametrize("T,H,E,I,K", [(40, 512, 64, 384, 6), (100, 256, 60, 96, 6), (100, 1024, 128, 256, 8), (400, 512, 64, 512, 6)])
+def test_many_passes_give_the_same_bits(T, H, E, I, K):
+    """Every CTA works through items of groups of all sizes (one row to several tiles), over many passes: the pipelines'
+    barriers are passed millions of times without a wait that expires or a sum that differs."""
+    t = _fp8_weights(E, H, I, 0, T + E)
+    ids, tw = _spread_routing(T, E, K, T)
+    x = torch.randn((T, H), generator=_gen(T + 1), device="cuda").to(torch.bfloat16)
+    d = moe.Desc(T=T, H=H, E=E, I=I, top_k=K, w_dtype="fp8")
+    ws = torch.empty(moe.workspace_bytes(d), dtype=torch.uint8, device="cuda")
+    w = moe.Weights(**t)
+    first = _experts(d, x, t, ids, tw)
+    _ok()
+    want, tol = _expected(x, ids, tw, None, t, E, "silu")
+    assert torch.all((first.double() - want).abs() <= tol)
+    out = torch.empty_like(first)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(400):
+        moe.experts(d, x, w, ids, tw, out, ws)
+        differ += (out != first).sum()
+    _ok()
+    assert int(differ) == 0
+
+
+@pytest.mark.parametrize("T,E,K", [(8, 4, 2), (24, 16, 4), (60, 4, 2), (300, 4, 2)])  # each form of the product
+def test_wait_timeout_is_reported_and_context_survives(T, E, K):
+    """One stage of CTA 0 is left unfilled: its waits run out, the error is reported and the next call is right."""
+    H, I = 512, 256
+    t = _fp8_weights(E, H, I, 0, 71)
+    g = _gen(72)
+    x = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+    ids = torch.rand((T, E), generator=g, device="cuda").topk(K, 1).indices.to(torch.int32)
+    tw = torch.rand((T, K), generator=g, device="cuda")
+    d = moe.Desc(T=T, H=H, E=E, I=I, top_k=K, w_dtype="fp8")
+    clean = _experts(d, x, t, ids, tw)
+    _ok()
+    a, sa, b, sb = _operands(T, 1, H, I, "e4m3", "e4m3", 73)
+    product = _product(a, sa, b, sb, None, torch.float32)
+    out = torch.empty_like(clean)
+    y = torch.empty_like(product)
+    try:
+        moe.debug_set_wait_limit(20_000_000)  # about 10 ms of SM cycles
+        moe.debug_set_skip_stage(True)
+        _experts(d, x, t, ids, tw, out=out)
+        torch.cuda.synchronize()
+        assert moe.last_device_status() == moe.MOE_ERR_TIMEOUT
+        moe.fp8_gemm(a, sa, b, sb, y)
+        torch.cuda.synchronize()
+        assert moe.last_device_status() == moe.MOE_ERR_TIMEOUT
+    finally:
+        moe.debug_set_skip_stage(False)
+        moe.debug_set_wait_limit(0)
+    assert torch.equal(_experts(d, x, t, ids, tw), clean)
+    assert torch.equal(_product(a, sa, b, sb, None, torch.float32), product)
+    _ok()
+
+
+def test_layer_host():
+    """The layer from and to pinned host memory, with fp8 experts."""
+    T, H, E, I, K = 33, 256, 8, 128, 2
+    g = _gen(75)
+    t = _fp8_weights(E, H, I, 0, 76)
+    d = moe.Desc(T=T, H=H, E=E, I=I, top_k=K, w_dtype="fp8", router_dtype="f32")
+    w = moe.Weights(router=(torch.randn((E, H), generator=g, device="cuda") / 16), **t)
+    x = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+    ws = torch.empty(moe.workspace_bytes(d), dtype=torch.uint8, device="cuda")
+    want = torch.empty_like(x)
+    moe.layer(d, x, w, want, ws)
+    _ok()
+    xh, oh = x.cpu().pin_memory(), torch.empty((T, H), dtype=torch.bfloat16).pin_memory()
+    moe.layer_host(d, xh, w, oh, torch.empty_like(x), torch.empty_like(x), ws)
+    _ok()
+    assert torch.equal(oh, want.cpu())
+
+
+def test_quantize_in_a_graph():
+    x = torch.randn((40, 416), generator=_gen(77), device="cuda")
+    w = torch.randn((2, 96, 416), generator=_gen(78), device="cuda")
+    q, s = torch.empty((40, 416), dtype=FMT["e4m3"], device="cuda"), torch.empty((4, 40), device="cuda")
+    qw, sw = torch.empty((2, 96, 416), dtype=FMT["e4m3"], device="cuda"), torch.empty((2, 1, 4), device="cuda")
+    off = torch.tensor([0, 11, 40], dtype=torch.int32, device="cuda")
+    y = torch.empty((40, 96), device="cuda")
+
+    def run():
+        moe.fp8_quantize(x, q, s)
+        moe.fp8_quantize_weights(w, qw, sw)
+        moe.fp8_gemm(q, s, qw, sw, y, offsets=off)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for i in range(3):
+        x.copy_(torch.randn(x.shape, generator=_gen(79 + i), device="cuda"))
+        w.copy_(torch.randn(w.shape, generator=_gen(89 + i), device="cuda"))
+        graph.replay()
+        _ok()
+        got = y.clone()
+        run()
+        _ok()
+        assert torch.equal(got, y)
+        _check_product(got, q, s, qw, sw, [0, 11, 40])

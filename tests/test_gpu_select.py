@@ -223,3 +223,29 @@ def test_far_rows():
     l = buf.as_strided((T, E), (ld, 1))
     l.copy_(torch.randn((T, E), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda"))
     _check(l, 4)
+
+
+def test_forward_and_backward_in_a_graph():
+    T, E, K = 70, 48, 4
+    d = moe.SelectDesc(T=T, E=E, top_k=K, scoring="sigmoid", renormalize=True)
+    l, dw = torch.randn((T, E), device="cuda"), torch.randn((T, K), device="cuda")
+    ids, w = torch.empty((T, K), dtype=torch.int32, device="cuda"), torch.empty((T, K), device="cuda")
+    dl = torch.empty((T, E), device="cuda")
+
+    def run():
+        moe.select(d, l, ids, w)
+        moe.select_backward(d, l, ids, dw, dl)
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for i in range(3):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        l.copy_(torch.randn((T, E), generator=g, device="cuda"))
+        dw.copy_(torch.randn((T, K), generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [v.clone() for v in (ids, w, dl)]
+        run()
+        assert all(torch.equal(a, b) for a, b in zip(got, (ids, w, dl)))
+    assert moe.last_device_status() == moe.MOE_OK
