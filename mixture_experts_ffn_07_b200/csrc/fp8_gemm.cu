@@ -14,11 +14,11 @@
 // A k-block of 128 is four MMAs of K = 32 into one of the TMEM accumulators; the epilogue warps read each finished
 // k-block out of TMEM and add it, scaled, to f32 registers while the next ones run.
 //  * warp 0: TMA producer (weight tiles 128 x 128 bytes; token rows in boxes of 32, 128-byte swizzle, or, for the
-//    routed gate/up of small batches, gathered row by row straight from the tokens with tile::gather4);
-//  * warp 1: allocates TMEM, issues tcgen05.mma kind::f8f6f4 from one lane; with tiles of 32 rows warp 3 issues every
-//    second k-block: each has an accumulator of its own, and a k-block costs its issuer two barrier waits, four
+//    routed gate/up, gathered row by row straight from the tokens with tile::gather4);
+//  * warp 1: allocates TMEM, issues tcgen05.mma kind::f8f6f4 from one lane; warp 3 issues every second k-block: each
+//    has an accumulator of its own, and a k-block costs its issuer two barrier waits, four
 //    instructions and a commit, 600-800 cycles, more than its copies take;
-//  * warp 2 (and 3 with tiles of 64): loads the scales of each k-block, multiplies row and tile scale, into a ring;
+//  * warp 2: loads the scales of each k-block, multiplies row and tile scale, into a ring;
 //  * warps 4-11: epilogue; warp w reads TMEM lanes 32 (w % 4), and one half of the columns, or, with at most 16 rows,
 //    every second k-block.
 // A k-block's stage and accumulator have the same number, and one commit frees the stage and fills the accumulator.
@@ -34,11 +34,14 @@ namespace moe {
 
 namespace {
 
-constexpr int BOX = 32;            // token rows per TMA box
+constexpr int NT = 32;             // token rows of a tile, one TMA box
+constexpr int HALF = NT / 2;       // columns per epilogue warp
+constexpr int X = HALF / 8;        // 8-column groups per TMEM load
+constexpr int MMA_WARPS = 2;
 constexpr int PITCH8 = 144;        // dual: staged bytes per row of codes (128 used)
 constexpr int PITCH16 = 80;        // single: staged bytes per row of 32 bf16 outputs (64 used)
 
-template <bool DUAL, int NT>
+template <bool DUAL>
 struct Cfg {
   static constexpr int MATS = DUAL ? 2 : 1;
   static constexpr int STAGE_BYTES = MATS * W_BYTES + NT * KB;
@@ -46,15 +49,10 @@ struct Cfg {
   // Stages, and accumulators.  An even number: a k-block's stage then always belongs to the same MMA warp and, with at
   // most 16 rows, to the same half of the epilogue, so each of them sees every phase of the barriers that it waits for
   // (waiting for a phase by its parity while the one before is still open would pass at once).
-  static constexpr int RING = NT == 32 && !DUAL ? 8 : 4;
+  static constexpr int RING = DUAL ? 4 : 8;
   static_assert(RING % 2 == 0, "phases");
-  static constexpr uint32_t TMEM_COLS = RING * ACC <= 256 ? 256 : 512;
-  static_assert(RING * ACC <= 512 && NT <= 64, "TMEM columns");
-  static constexpr int HALF = NT / 2;                        // columns per epilogue warp
-  static constexpr int X = HALF / 8 < 8 ? HALF / 8 : 8;      // 8-column groups per TMEM load
-  static constexpr int CHUNKS = HALF / (8 * X);
-  static constexpr int SCALE_WARPS = NT > 32 ? 2 : 1;
-  static constexpr int MMA_WARPS = NT > 32 ? 1 : 2;
+  static constexpr uint32_t TMEM_COLS = 256;
+  static_assert(RING * ACC <= 256, "TMEM columns");
   // Ring of scales.  The scale warps write a k-block's slot after its stage came free, that is after the MMA RING
   // k-blocks earlier, which the epilogue's reads of the k-block RING before that one (values and scales) precede: a
   // slot 2 RING k-blocks old is read, and the ring needs no barriers of its own.
@@ -68,18 +66,17 @@ struct Item {
   bool alone;          // the group has one token tile: its weights are read once
 };
 
-template <bool DUAL, int NT>
+template <bool DUAL>
 struct Aux {
-  alignas(16) float sc[Cfg<DUAL, NT>::SLOTS][DUAL ? 2 : 1][NT];  // row scale x tile scale
+  alignas(16) float sc[Cfg<DUAL>::SLOTS][DUAL ? 2 : 1][NT];  // row scale x tile scale
   alignas(16) float inv[DUAL ? NT : 4];           // dual: 1 / h scale of each column
   uint32_t red[DUAL ? EPI_WARPS : 1][NT / 2];     // dual: largest |h| of each warp's columns, as bits
   int dest[2][DUAL ? 4 : NT];                     // single: output row of each column (-1: none)
   float rscale[2][DUAL ? 4 : NT];
-  // tiles of 32 rows, at most 16 of them in use: the sums of the epilogue's second half
-  unsigned long long alt[NT == 32 ? Cfg<DUAL, NT>::MATS * 8 : 1][EPI_WARPS * 16];
-  uint64_t full[Cfg<DUAL, NT>::RING];
-  uint64_t done[Cfg<DUAL, NT>::RING];    // the k-block's MMAs: its stage is free and its accumulator full
-  uint64_t tempty[Cfg<DUAL, NT>::RING];
+  unsigned long long alt[Cfg<DUAL>::MATS * 8][EPI_WARPS * 16];  // at most 16 rows: the second half's sums
+  uint64_t full[Cfg<DUAL>::RING];
+  uint64_t done[Cfg<DUAL>::RING];    // the k-block's MMAs: its stage is free and its accumulator full
+  uint64_t tempty[Cfg<DUAL>::RING];
   uint64_t all_done;
   uint32_t tmem_base;
   int abort;
@@ -89,22 +86,13 @@ struct Aux {
   Item first;  // this CTA's first item
 };
 
-template <bool DUAL, int NT>
-constexpr size_t kSmem = 1024 + static_cast<size_t>(Cfg<DUAL, NT>::RING) * Cfg<DUAL, NT>::STAGE_BYTES +
-                         Cfg<DUAL, NT>::OUT_STAGE + sizeof(Aux<DUAL, NT>);
+template <bool DUAL>
+constexpr size_t kSmem = 1024 + static_cast<size_t>(Cfg<DUAL>::RING) * Cfg<DUAL>::STAGE_BYTES +
+                         Cfg<DUAL>::OUT_STAGE + sizeof(Aux<DUAL>);
 
 // 16 TMEM lanes x 8 X columns.  Group i of 8 columns: registers 4 i, 4 i + 1 hold columns 2 (lane % 4), + 1 of row
 // lane / 4, registers 4 i + 2, 4 i + 3 the same columns of row lane / 4 + 8.  So a thread needs two of the eight
 // column scales, not all of them (reading 32 lanes x 1 column instead cost one shared load per four products).
-__device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
 __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[8]) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -112,12 +100,6 @@ __device__ __forceinline__ void tmem_ld_16x256b(uint32_t taddr, uint32_t (&r)[8]
                : "memory");
 }
 // Waits for the thread's TMEM loads; names the registers, so that nothing reads them earlier.
-__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 ::"memory");
-}
 __device__ __forceinline__ void tmem_wait(uint32_t (&r)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
@@ -131,7 +113,7 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
 }
 
 // Item `local` of group g: its tiles of NT rows, every one against the same weight tile before the next weight tile.
-template <int NT, typename AuxT>
+template <typename AuxT>
 __device__ __forceinline__ Item item_at(const AuxT& aux, int g, int local) {
   Item it;
   it.g = g;
@@ -144,7 +126,7 @@ __device__ __forceinline__ Item item_at(const AuxT& aux, int g, int local) {
   it.n = min(NT, cnt - tt * NT);
   return it;
 }
-template <int NT, typename AuxT>
+template <typename AuxT>
 __device__ __forceinline__ Item decode_item(const AuxT& aux, int G, int w) {
   int lo = 0, hi = G - 1;
   while (lo < hi) {
@@ -154,7 +136,7 @@ __device__ __forceinline__ Item decode_item(const AuxT& aux, int G, int w) {
     else
       hi = mid - 1;
   }
-  return item_at<NT>(aux, lo, w - aux.item_off[lo]);
+  return item_at(aux, lo, w - aux.item_off[lo]);
 }
 
 // The two halves of a barrier over every thread of the cluster (whole warps); they order the shared-memory accesses
@@ -189,17 +171,17 @@ __device__ __forceinline__ uint32_t clusters() {
   return r;
 }
 
-template <bool DUAL, int NT>
+template <bool DUAL>
 __global__ void __launch_bounds__(THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapW0,
                     const __grid_constant__ CUtensorMap mapW1, const Params p) {
-  using C = Cfg<DUAL, NT>;
+  using C = Cfg<DUAL>;
   constexpr int RING = C::RING;
   constexpr int SLOTS = C::SLOTS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* out_stage = smem + RING * C::STAGE_BYTES;
-  Aux<DUAL, NT>& aux = *reinterpret_cast<Aux<DUAL, NT>*>(out_stage + C::OUT_STAGE);
+  Aux<DUAL>& aux = *reinterpret_cast<Aux<DUAL>*>(out_stage + C::OUT_STAGE);
   volatile int* abort_flag = &aux.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool split = p.split > 1;
@@ -208,11 +190,11 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < RING; ++s) {
-      mbar_init(&aux.full[s], 1 + C::SCALE_WARPS);
+      mbar_init(&aux.full[s], 2);  // the producer and the scale warp
       mbar_init(&aux.done[s], 1);
       mbar_init(&aux.tempty[s], EPI_WARPS);
     }
-    mbar_init(&aux.all_done, C::MMA_WARPS);
+    mbar_init(&aux.all_done, MMA_WARPS);
     aux.abort = 0;
     fence_mbar_init();
   } else if (threadIdx.x == 64) {
@@ -261,7 +243,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int i = 0; i < 8; ++i) {
       const int g = lane * 8 + i;
       if (g < p.G) aux.item_off[g] = run;
-      if (run <= first && first < run + v[i]) aux.first = item_at<NT>(aux, g, first - run);
+      if (run <= first && first < run + v[i]) aux.first = item_at(aux, g, first - run);
       run += v[i];
     }
     if (lane == 31) aux.item_off[p.G] = incl;
@@ -289,8 +271,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     for (int w = first; w < total; w += step) {
       ok = ok && !__shfl_sync(0xffffffffu, *abort_flag, 0);
       if (ok) {
-        const Item it = w == first ? aux.first : decode_item<NT>(aux, p.G, w);
-        const int quads = (it.n + 3) / 4, boxes = (it.n + BOX - 1) / BOX;
+        const Item it = w == first ? aux.first : decode_item(aux, p.G, w);
+        const int quads = (it.n + 3) / 4;
         const uint64_t pol_w = it.alone ? pol_first : pol_normal;
         int tok[4] = {0, 0, 0, 0};
         if (p.gather && lane < quads)
@@ -299,7 +281,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int t = p.a_scale_map[it.row0 + min(4 * lane + j, it.n - 1)] / p.a_scale_div;
             tok[j] = min(max(t, 0), static_cast<int>(p.a_ld) - 1);
           }
-        const int bytes = C::MATS * W_BYTES + (p.gather ? quads * 4 * KB : boxes * BOX * KB);
+        const int bytes = C::MATS * W_BYTES + (p.gather ? quads * 4 : NT) * KB;
         int done = 0;  // k-blocks of this item already requested
         if (w == first) {
           // The first item's first stages are free, and a lane fills each: waiting for and arriving on a barrier takes
@@ -325,9 +307,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             pol_last);
             }
           } else if (mine) {
-            for (int b = 0; b < boxes; ++b)
-              tma_load_2d_hint(st + C::MATS * W_BYTES + b * BOX * KB, &mapA, &aux.full[lane], x, it.row0 + b * BOX,
-                               pol_last);
+            tma_load_2d_hint(st + C::MATS * W_BYTES, &mapA, &aux.full[lane], x, it.row0, pol_last);
           }
           __syncwarp();
           outstanding = (1u << fill) - 1u;
@@ -353,8 +333,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (p.gather) {
             if (lane < quads)
               tma_gather4(sa + lane * 4 * KB, &mapA, &aux.full[s], kb * KB, tok[0], tok[1], tok[2], tok[3], pol_last);
-          } else if (lane < boxes) {
-            tma_load_2d_hint(sa + lane * BOX * KB, &mapA, &aux.full[s], kb * KB, it.row0 + lane * BOX, pol_last);
+          } else if (lane == 0) {
+            tma_load_2d_hint(sa, &mapA, &aux.full[s], kb * KB, it.row0, pol_last);
           }
           outstanding |= 1u << s;
           out_phase = (out_phase & ~(1u << s)) | (ph << s);
@@ -366,18 +346,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0 && *abort_flag)  // let issued copies land before the CTA exits
       for (int s = 0; s < RING; ++s)
         if (outstanding & (1u << s)) wait_cycles(&aux.full[s], (out_phase >> s) & 1u, limit);
-  } else if (warp == 1 || (warp == 3 && C::MMA_WARPS == 2)) {
+  } else if (warp == 1 || warp == 3) {
     // ---------------------------------------------------------- MMA issuers (one lane; k-blocks in turn)
     const uint32_t mine = warp >> 1;
     uint32_t kbg = 0;
     bool ok = true;
     for (int w = first; w < total; w += step) {
       if (lane == 0 && ok) {
-        const Item it = w == first ? aux.first : decode_item<NT>(aux, p.G, w);
+        const Item it = w == first ? aux.first : decode_item(aux, p.G, w);
         const uint32_t n16 = (it.n + 15) & ~15;
         const uint32_t idesc = p.idesc | ((n16 >> 3) << 17);
         for (int kb = kb_lo; kb < kb_hi; ++kb, ++kbg) {
-          if (C::MMA_WARPS == 2 && (kbg & 1u) != mine) continue;
+          if ((kbg & 1u) != mine) continue;
           const int s = kbg % RING;
           const uint32_t round = kbg / RING;
           if ((round > 0 && !mbar_wait_bounded(&aux.tempty[s], (round & 1u) ^ 1u, limit, abort_flag)) ||
@@ -406,30 +386,24 @@ __global__ void __launch_bounds__(THREADS, 1)
       umma_commit(&aux.all_done);  // every MMA issued completes before TMEM is released
       wait_cycles(&aux.all_done, 0, limit);
     }
-  } else if (warp < 4) {
-    // ---------------------------------------------------------- scales: warp 2 + i has the i-th part of the columns.
-    // AHEAD k-blocks are in flight per warp (a load takes about 1000 cycles).
-    constexpr int PER = NT / 32 / C::SCALE_WARPS, AHEAD = 4;
-    const int col0 = (warp - 2) * 32 * PER + lane;
+  } else if (warp == 2) {
+    // ---------------------------------------------------------- scales: AHEAD k-blocks are in flight (a load takes
+    // about 1000 cycles)
+    constexpr int AHEAD = 4;
     uint32_t kbg = 0;
-    bool ok = warp - 2 < C::SCALE_WARPS;
+    bool ok = true;
     if (p.early) pdl_wait();
     for (int w = first; w < total; w += step) {
       if (ok) {
-        const Item it = w == first ? aux.first : decode_item<NT>(aux, p.G, w);
-        int at[PER];
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const int r = it.row0 + min(col0 + 32 * j, it.n - 1);
-          const int col = p.a_scale_map ? p.a_scale_map[r] / p.a_scale_div : r;
-          at[j] = min(max(col, 0), static_cast<int>(p.a_ld) - 1);
-        }
+        const Item it = w == first ? aux.first : decode_item(aux, p.G, w);
+        const int r = it.row0 + min(lane, it.n - 1);
+        const int col = p.a_scale_map ? p.a_scale_map[r] / p.a_scale_div : r;
+        const int at = min(max(col, 0), static_cast<int>(p.a_ld) - 1);
         const long long sb = (static_cast<long long>(it.g) * p.n_tiles + it.wt) * nkb_all;
-        float v[AHEAD][PER], t0[AHEAD], t1[AHEAD];
+        float v[AHEAD], t0[AHEAD], t1[AHEAD];
         auto load = [&](int kb, int b) {
           const int k = min(kb, nkb_all - 1);
-#pragma unroll
-          for (int j = 0; j < PER; ++j) v[b][j] = __ldg(p.a_scale + k * p.a_ld + at[j]);
+          v[b] = __ldg(p.a_scale + k * p.a_ld + at);
           t0[b] = __ldg(p.s0 + sb + k);
           t1[b] = DUAL ? __ldg(p.s1 + sb + k) : 0.f;
         };
@@ -446,11 +420,8 @@ __global__ void __launch_bounds__(THREADS, 1)
               break;
             }
             const int slot = kbg % SLOTS;
-#pragma unroll
-            for (int j = 0; j < PER; ++j) {
-              aux.sc[slot][0][col0 + 32 * j] = v[b][j] * t0[b];
-              if (DUAL) aux.sc[slot][C::MATS - 1][col0 + 32 * j] = v[b][j] * t1[b];
-            }
+            aux.sc[slot][0][lane] = v[b] * t0[b];
+            if (DUAL) aux.sc[slot][C::MATS - 1][lane] = v[b] * t1[b];
             load(kb0 + b + AHEAD, b);
             __syncwarp();
             if (lane == 0) mbar_arrive(&aux.full[s]);
@@ -462,8 +433,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else {
     // ---------------------------------------------------------- epilogue
-    constexpr int HALF = C::HALF, X = C::X, CHUNKS = C::CHUNKS, MATS = C::MATS;
-    constexpr int STEPS = MATS * CHUNKS * 2;  // TMEM loads per k-block: (matrix, column chunk, 16-lane half)
+    constexpr int MATS = C::MATS;
+    constexpr int STEPS = MATS * 2;  // TMEM loads per k-block: (matrix, 16-lane half)
     const int ew = warp - 4;
     const int q = warp & 3, half = ew >> 2;
     const int et = threadIdx.x - 128;  // thread of the epilogue
@@ -474,10 +445,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     bool alive = true;
     if (p.early) pdl_wait();
     for (int w = first; w < total; w += step, parity ^= 1) {
-      const Item it = w == first ? aux.first : decode_item<NT>(aux, p.G, w);
+      const Item it = w == first ? aux.first : decode_item(aux, p.G, w);
       const int wt = it.wt;
       const int n16 = (it.n + 15) & ~15;
-      const bool alt = NT == 32 && it.n <= 16;  // the halves take k-blocks in turn, both the first 16 columns
+      const bool alt = it.n <= 16;  // the halves take k-blocks in turn, both the first 16 columns
       const int col0 = alt ? 0 : half * HALF;
       if (!DUAL) {  // output row and scale of each column
         for (int c = et; c < NT; c += EPI_WARPS * 32) {
@@ -496,14 +467,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           aux.rscale[parity][c] = rs;
         }
       }
-      // acc[m][chunk][half of the lanes][2 i + b]: columns 8 (chunk X + i) + lc, + 1 of row 16 half + 8 b + lr
-      unsigned long long acc[MATS][CHUNKS][2][2 * X];
+      // acc[m][half of the lanes][2 i + b]: columns 8 i + lc, + 1 of row 16 half + 8 b + lr
+      unsigned long long acc[MATS][2][2 * X];
 #pragma unroll
       for (int m = 0; m < MATS; ++m)
 #pragma unroll
-        for (int c = 0; c < CHUNKS; ++c)
-#pragma unroll
-          for (int j = 0; j < 2 * X; ++j) acc[m][c][0][j] = acc[m][c][1][j] = 0ull;
+        for (int j = 0; j < 2 * X; ++j) acc[m][0][j] = acc[m][1][j] = 0ull;
       bool ok = alive;
       for (int kb = kb_lo; kb < kb_hi && ok; ++kb, ++kbg) {
         // (the barrier after the item's last k-block closes the phases that the other half has waited for)
@@ -519,19 +488,19 @@ __global__ void __launch_bounds__(THREADS, 1)
           unsigned long long sc[X];
 #pragma unroll
           for (int st = 0; st < STEPS; ++st) {
-            const int m = st / (2 * CHUNKS), c = st / 2 % CHUNKS, r = st & 1;
+            const int m = st >> 1, r = st & 1;
             uint32_t v[4 * X];
-            tmem_ld_16x256b(tb + (static_cast<uint32_t>(16 * r) << 16) + m * NT + c * 8 * X, v);
+            tmem_ld_16x256b(tb + (static_cast<uint32_t>(16 * r) << 16) + m * NT, v);
             if (r == 0) {
 #pragma unroll
               for (int i = 0; i < X; ++i)
-                sc[i] = *reinterpret_cast<const unsigned long long*>(&aux.sc[slot][m][col0 + 8 * (c * X + i) + lc]);
+                sc[i] = *reinterpret_cast<const unsigned long long*>(&aux.sc[slot][m][col0 + 8 * i + lc]);
             }
             tmem_wait(v);
 #pragma unroll
             for (int i = 0; i < X; ++i) {
-              fma2(acc[m][c][r][2 * i], v[4 * i], v[4 * i + 1], sc[i]);
-              fma2(acc[m][c][r][2 * i + 1], v[4 * i + 2], v[4 * i + 3], sc[i]);
+              fma2(acc[m][r][2 * i], v[4 * i], v[4 * i + 1], sc[i]);
+              fma2(acc[m][r][2 * i + 1], v[4 * i + 2], v[4 * i + 3], sc[i]);
             }
           }
         }
@@ -545,8 +514,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       // uniform over the epilogue: either every warp has all k-blocks or the tile is dropped; also orders dest
       alive = named_barrier_and(1, EPI_WARPS * 32, ok);
       if (alt) {
-        constexpr int VALS = MATS * CHUNKS * 4 * X;
-        unsigned long long* flat = &acc[0][0][0][0];
+        constexpr int VALS = MATS * 4 * X;
+        unsigned long long* flat = &acc[0][0][0];
         unsigned long long* at = &aux.alt[0][et & 127];
         if (half)
 #pragma unroll
@@ -560,10 +529,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         // order.  Distributed shared memory passes about 20 bytes a cycle, so only columns in use are read; a plain
         // product is added and written by all the CTAs, each a part of the values, h by the first one, which needs
         // whole columns for their scales.
-        constexpr int VALS = MATS * CHUNKS * 4 * X, PITCH = EPI_WARPS * 32;
+        constexpr int VALS = MATS * 4 * X, PITCH = EPI_WARPS * 32;
         static_assert(VALS * PITCH * 8 <= RING * C::STAGE_BYTES, "partial sums");
         unsigned long long* mine = reinterpret_cast<unsigned long long*>(smem) + et;
-        unsigned long long* flat = &acc[0][0][0][0];  // value j: columns 8 ((j / 2) % X) + lc, + 1 of a row
+        unsigned long long* flat = &acc[0][0][0];  // value j: columns 8 ((j / 2) % X) + lc, + 1 of a row
 #pragma unroll
         for (int j = 0; j < VALS; ++j) mine[j * PITCH] = flat[j];
         cluster_arrive();
@@ -627,39 +596,25 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int rb = 0; rb < 4; ++rb) {
             float g0, g1, u0, u1;
-            split2(acc[0][0][rb >> 1][2 * i + (rb & 1)], g0, g1);
-            split2(acc[MATS - 1][0][rb >> 1][2 * i + (rb & 1)], u0, u1);
+            split2(acc[0][rb >> 1][2 * i + (rb & 1)], g0, g1);
+            split2(acc[MATS - 1][rb >> 1][2 * i + (rb & 1)], u0, u1);
             const float h0 = act_fast(ac, g0) * u0, h1 = act_fast(ac, g1) * u1;
-            acc[0][0][rb >> 1][2 * i + (rb & 1)] = join2(h0, h1);
+            acc[0][rb >> 1][2 * i + (rb & 1)] = join2(h0, h1);
             mx[2 * i] = max(mx[2 * i], __float_as_uint(h0) & 0x7fffffffu);
             mx[2 * i + 1] = max(mx[2 * i + 1], __float_as_uint(h1) & 0x7fffffffu);
           }
         }
-        // over the warp's 32 rows: halve the columns a lane keeps while exchanging with lanes 16, 8, 4 away
-        int base = 0;
+        // over the warp's 32 rows: halve the columns a lane keeps while exchanging with lanes 16 and 8 away
+        static_assert(X == 2, "four columns a thread");
+        const bool up16 = lane & 16, up8 = lane & 8;
 #pragma unroll
-        for (int b = 0; b < 3; ++b) {
-          constexpr int N0 = 2 * X;
-          const int keep = N0 >> (b + 1);
-          const int o = 16 >> b;
-          const bool upper = lane & o;
-          if (keep > 0) {
-#pragma unroll
-            for (int j = 0; j < keep; ++j) {
-              const uint32_t give = upper ? mx[j] : mx[j + keep], take = upper ? mx[j + keep] : mx[j];
-              mx[j] = max(take, __shfl_xor_sync(0xffffffffu, give, o));
-            }
-            base += upper ? keep : 0;
-          } else {
-            mx[0] = max(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], o));
-          }
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t give = up16 ? mx[j] : mx[j + 2], keep = up16 ? mx[j + 2] : mx[j];
+          mx[j] = max(keep, __shfl_xor_sync(0xffffffffu, give, 16));
         }
-        constexpr int LEFT = 2 * X / 8 > 1 ? 2 * X / 8 : 1;
-#pragma unroll
-        for (int j = 0; j < LEFT; ++j) {
-          const int k = base + j;  // the thread's column k: group k / 2, parity k % 2
-          aux.red[ew][8 * (k >> 1) + lc + (k & 1)] = mx[j];
-        }
+        uint32_t top = max(up8 ? mx[1] : mx[0], __shfl_xor_sync(0xffffffffu, up8 ? mx[0] : mx[1], 8));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 4));
+        aux.red[ew][(up16 ? 8 : 0) + lc + (up8 ? 1 : 0)] = top;
         named_barrier(2 + half, 128);
         if (et - half * 128 < HALF) {
           const int c = et - half * 128;
@@ -681,7 +636,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int rb = 0; rb < 4; ++rb) {
             float h0, h1;
-            split2(acc[0][0][rb >> 1][2 * i + (rb & 1)], h0, h1);
+            split2(acc[0][rb >> 1][2 * i + (rb & 1)], h0, h1);
             const uint32_t code = fp8_pack2(h0 * inv.x, h1 * inv.y, MOE_E4M3);
             o[8 * rb] = static_cast<uint8_t>(code);
             o[8 * rb + PITCH8] = static_cast<uint8_t>(code >> 8);
@@ -691,43 +646,38 @@ __global__ void __launch_bounds__(THREADS, 1)
         // whole rows of 128 codes: eight lanes a row
         const int ch = et & 7;
         if (wt * WM + ch * 16 < p.N) {
-#pragma unroll
-          for (int c0 = 0; c0 < HALF; c0 += 16) {
-            const int c = c0 + ((et & 127) >> 3);
-            const int col = half * HALF + c;
-            if (col < it.n)
-              *reinterpret_cast<uint4*>(p.out_q + static_cast<long long>(it.row0 + col) * p.N + wt * WM + ch * 16) =
-                  *reinterpret_cast<const uint4*>(stage + c * PITCH8 + ch * 16);
-          }
+          const int c = (et & 127) >> 3;
+          const int col = half * HALF + c;
+          if (col < it.n)
+            *reinterpret_cast<uint4*>(p.out_q + static_cast<long long>(it.row0 + col) * p.N + wt * WM + ch * 16) =
+                *reinterpret_cast<const uint4*>(stage + c * PITCH8 + ch * 16);
         }
       } else if (wt * WM + q * 32 < p.N) {  // N is a multiple of 32: the warp's rows are all inside or all outside
         if (p.out_bf16) {
-          // 16 columns at a time through the warp's staging rows: [column][32 rows] bf16
+          // the 16 columns through the warp's staging rows: [column][32 rows] bf16
           uint8_t* stage = out_stage + ew * 16 * PITCH16;
           const uint32_t st_addr = smem_addr(stage) + (lane & 7) * PITCH16 + (lane >> 3) * 16;
           const int ch = lane & 3;
+          if (half * HALF < it.n) {  // warp-uniform
 #pragma unroll
-          for (int i = 0; i < CHUNKS * X; i += 2) {
-            if (half * HALF + 8 * i >= it.n) break;  // warp-uniform
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int i = 0; i < X; ++i) {
               uint32_t pk[4];
-              const int col = half * HALF + 8 * (i + e) + lc;
+              const int col = half * HALF + 8 * i + lc;
               const float s0 = aux.rscale[parity][col], s1 = aux.rscale[parity][col + 1];
 #pragma unroll
               for (int rb = 0; rb < 4; ++rb) {
                 float y0, y1;
-                split2(acc[0][(i + e) / X][rb >> 1][2 * ((i + e) % X) + (rb & 1)], y0, y1);
+                split2(acc[0][rb >> 1][2 * i + (rb & 1)], y0, y1);
                 const __nv_bfloat162 t = __floats2bfloat162_rn(y0 * s0, y1 * s1);
                 pk[rb] = *reinterpret_cast<const uint32_t*>(&t);
               }
-              stmatrix_x4_trans(st_addr + e * 8 * PITCH16, pk[0], pk[1], pk[2], pk[3]);
+              stmatrix_x4_trans(st_addr + i * 8 * PITCH16, pk[0], pk[1], pk[2], pk[3]);
             }
             __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const int c = 8 * e + lr;
-              const int d = aux.dest[parity][half * HALF + 8 * i + c];
+            for (int i = 0; i < X; ++i) {
+              const int c = 8 * i + lr;
+              const int d = aux.dest[parity][half * HALF + c];
               const uint4 v = *reinterpret_cast<const uint4*>(stage + c * PITCH16 + ch * 16);
               if (d >= 0)
                 *reinterpret_cast<uint4*>(p.out_bf16 + static_cast<long long>(d) * p.N + wt * WM + q * 32 + ch * 8) = v;
@@ -736,7 +686,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < CHUNKS * X; ++i) {
+          for (int i = 0; i < X; ++i) {
             const int col = half * HALF + 8 * i + lc;
             const int d0 = aux.dest[parity][col], d1 = aux.dest[parity][col + 1];
             const float s0 = aux.rscale[parity][col], s1 = aux.rscale[parity][col + 1];
@@ -744,7 +694,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int rb = 0; rb < 4; ++rb) {
               float y0, y1;
-              split2(acc[0][i / X][rb >> 1][2 * (i % X) + (rb & 1)], y0, y1);
+              split2(acc[0][rb >> 1][2 * i + (rb & 1)], y0, y1);
               if (d0 >= 0) o[static_cast<long long>(d0) * p.N + 8 * rb] = y0 * s0;
               if (d1 >= 0) o[static_cast<long long>(d1) * p.N + 8 * rb] = y1 * s1;
             }
@@ -770,7 +720,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // ------------------------------------------------------------------ host side
 // Clusters of `size` CTAs of the kernel that fit on the device at once, asked for once per device.
-template <bool DUAL, int NT>
+template <bool DUAL>
 int resident_clusters(const Ctx& c, int size) {
   constexpr int kMaxDevices = 64;
   static std::atomic<int> cached[kMaxDevices][9];  // 1 + the number
@@ -780,7 +730,7 @@ int resident_clusters(const Ctx& c, int size) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(size * (c.num_sms / size));
   cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = kSmem<DUAL, NT>;
+  cfg.dynamicSmemBytes = kSmem<DUAL>;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = size;
@@ -788,7 +738,7 @@ int resident_clusters(const Ctx& c, int size) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<DUAL, NT>, &cfg) != cudaSuccess) n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, fp8_gemm_kernel<DUAL>, &cfg) != cudaSuccess) n = 0;
   cudaGetLastError();
   cached[dev][size].store(n + 1);
   return n;
@@ -797,31 +747,31 @@ int resident_clusters(const Ctx& c, int size) {
 // How many CTAs share an item's k-blocks: as many (up to 8, of two k-blocks at least each) as leave every item's
 // cluster resident at once.  Clusters do not fill the GPU (148 SMs hold 74 of two CTAs, but 45 of three, 15 of eight),
 // and a second wave of them costs more than a wider split gains.
-template <bool DUAL, int NT>
+template <bool DUAL>
 void set_split(const Ctx& c, Params& p, long long items) {
   const int nkb = (p.K + KB - 1) / KB;
   for (int want = static_cast<int>(std::min<long long>({8LL, c.num_sms / std::max(1LL, items), nkb / 2})); want > 1; --want)
-    if (resident_clusters<DUAL, NT>(c, want) >= items) {
+    if (resident_clusters<DUAL>(c, want) >= items) {
       p.kb_per = (nkb + want - 1) / want;
       p.split = (nkb + p.kb_per - 1) / p.kb_per;
       return;
     }
 }
 
-template <bool DUAL, int NT>
+template <bool DUAL>
 cudaError_t launch_typed(const Ctx& c, const Fp8GemmArgs& a) {
   CUtensorMap mA, m0, m1;
-  if (!make_maps(a, a.gather ? 1 : BOX, &mA, &m0, &m1)) return cudaErrorInvalidValue;
+  if (!make_maps(a, a.gather ? 1 : NT, &mA, &m0, &m1)) return cudaErrorInvalidValue;
   Params p = make_params(c, a, a.b_fmt, a.a_fmt, WM);
   const long long tiles = a.rows / NT + std::min(a.G, a.rows);  // no fewer than there can be
   const long long items = tiles * p.n_tiles;
   p.early = a.early;
-  auto kern = fp8_gemm_kernel<DUAL, NT>;
-  constexpr size_t smem = kSmem<DUAL, NT>;
+  auto kern = fp8_gemm_kernel<DUAL>;
+  constexpr size_t smem = kSmem<DUAL>;
   static_assert(smem <= SMEM_MAX, "shared memory");
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  if (NT == 32) set_split<DUAL, NT>(c, p, items);
+  set_split<DUAL>(c, p, items);
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(c.num_sms / p.split, items) * p.split));
   cfg.blockDim = dim3(THREADS);
@@ -842,22 +792,23 @@ cudaError_t launch_typed(const Ctx& c, const Fp8GemmArgs& a) {
 
 // Mean rows of a group, of the groups that can hold any.
 double mean_rows(int rows, int G) { return static_cast<double>(rows) / std::max(1, std::min(G, rows)); }
-constexpr double kSmallRows = 16.0;
+// Up to how many of them this form is the faster one.  Measured on whole passes of the experts (64 experts of 2816 x 704,
+// 64 of 1024 x 2048, 16 of 2048 x 1024, 128 of 2048 x 768; us here / in fp8_gemm_rows.cu): the dual product with 14 rows a
+// group 89 / 94, 89 / 90, 32 / 37, 124 / 124 (with 20 rows the other one, by 1 to 5 us); the single one with 6 rows
+// 82 / 85, 79 / 81, 34 / 33, 108 / 110, with 10 rows 88 / 88, 82 / 84, 35 / 33, 126 / 123.
+constexpr double kSmallRowsDual = 16.0, kSmallRows = 8.0;
 
 }  // namespace
 
-bool fp8_gemm_gathers(int rows, int G) { return mean_rows(rows, G) <= kSmallRows; }
+bool fp8_gemm_gathers(int rows, int G) { return mean_rows(rows, G) <= kSmallRowsDual; }
 
 cudaError_t launch_fp8_gemm(const Ctx& c, const Fp8GemmArgs& a) {
   if (a.rows <= 0 || a.G <= 0) return cudaSuccess;
   if (a.G > MAX_G || a.N % 32 || a.K % 32 || a.N <= 0 || a.K <= 0) return cudaErrorInvalidValue;
-  // Measured crossovers with fp8_gemm_rows.cu (64 experts, K and N of 1024 and 2048): gate/up 62 us here and 71 us
-  // there at 48 rows a group, 76 and 72 us at 64; down 37 and 35 us at 16, 41 and 35 us at 24.
   const double rows = mean_rows(a.rows, a.G);
-  if (a.gather && rows > kSmallRows) return cudaErrorInvalidValue;
-  if (rows > (a.dual ? 48.0 : kSmallRows)) return launch_fp8_rows_gemm(c, a);
-  if (!a.dual) return launch_typed<false, 32>(c, a);
-  return rows > kSmallRows ? launch_typed<true, 64>(c, a) : launch_typed<true, 32>(c, a);
+  if (a.gather && (!a.dual || rows > kSmallRowsDual)) return cudaErrorInvalidValue;
+  if (rows > (a.dual ? kSmallRowsDual : kSmallRows)) return launch_fp8_rows_gemm(c, a);
+  return a.dual ? launch_typed<true>(c, a) : launch_typed<false>(c, a);
 }
 
 }  // namespace moe

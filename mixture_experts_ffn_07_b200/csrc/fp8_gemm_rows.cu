@@ -130,7 +130,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_alloc(&aux.tmem_base, TMEM_COLS);
     tmem_relinquish();
   }
-  pdl_wait();
+  // p.early: as in fp8_gemm.cu, the weights' copies start before the launch before has ended
+  if (!p.early) pdl_wait();
   pdl_trigger();
   for (int g = threadIdx.x; g < p.G; g += THREADS) {
     const int o0 = p.offsets ? p.offsets[g] : 0;
@@ -184,26 +185,39 @@ __global__ void __launch_bounds__(THREADS, 1)
       bool skipped = false;
       const uint64_t pol_a = l2_policy_evict_last();    // rows: read by every weight tile
       const uint64_t pol_w = l2_policy_evict_normal();  // weights: read by every row tile of the group
+      auto weights = [&](const Item& it, int n0, int kb, int s) {  // and the bytes of the whole stage
+        uint8_t* st = smem + s * STAGE_BYTES;
+        mbar_arrive_expect_tx(&aux.full[s], STAGE_BYTES);
+        tma_load_3d(st + W_BYTES, &mapW0, &aux.full[s], kb * KB, n0, it.g, pol_w);
+        tma_load_3d(st + 2 * W_BYTES, DUAL ? &mapW1 : &mapW0, &aux.full[s], kb * KB, DUAL ? n0 : n0 + WM, it.g, pol_w);
+      };
       for (int w = blockIdx.x; w < total; w += gridDim.x) {
         if (__shfl_sync(0xffffffffu, *abort_flag, 0)) break;
         const Item it = decode_item(aux, p.G, w);
         const int n0 = DUAL ? it.wt * WM : 2 * it.wt * WM;
+        int filled = 0;  // k-blocks whose weights are on their way
+        if (p.early && w == static_cast<int>(blockIdx.x)) {
+          filled = min(STAGES, nkb);
+          if (lane == 0)
+            for (int kb = 0; kb < filled; ++kb) {
+              if (p.skip_stage && kb == 0 && blockIdx.x == 0) continue;  // debug: leave this stage unfilled
+              weights(it, n0, kb, kb);
+            }
+          pdl_wait();
+        }
         if (lane == 0)
           for (int kb = 0; kb < nkb; ++kb, ++kbg) {
             const int s = kbg % STAGES;
             const uint32_t ph = (kbg / STAGES) & 1u;
-            if (!mbar_wait_bounded(&aux.empty[s], ph ^ 1u, limit, abort_flag)) break;
+            // (every stage whose weights are on their way gets its rows too, so that its copies are waited for)
+            if (kb >= filled && !mbar_wait_bounded(&aux.empty[s], ph ^ 1u, limit, abort_flag)) break;
             outstanding &= ~(1u << s);
             if (p.skip_stage && !skipped && blockIdx.x == 0) {  // debug: leave this stage unfilled
               skipped = true;
               continue;
             }
-            uint8_t* st = smem + s * STAGE_BYTES;
-            mbar_arrive_expect_tx(&aux.full[s], STAGE_BYTES);
-            tma_load_2d_hint(st, &mapA, &aux.full[s], kb * KB, it.row0, pol_a);
-            tma_load_3d(st + W_BYTES, &mapW0, &aux.full[s], kb * KB, n0, it.g, pol_w);
-            tma_load_3d(st + 2 * W_BYTES, DUAL ? &mapW1 : &mapW0, &aux.full[s], kb * KB, DUAL ? n0 : n0 + WM, it.g,
-                        pol_w);
+            if (kb >= filled) weights(it, n0, kb, s);
+            tma_load_2d_hint(smem + s * STAGE_BYTES, &mapA, &aux.full[s], kb * KB, it.row0, pol_a);
             outstanding |= 1u << s;
             out_phase = (out_phase & ~(1u << s)) | (ph << s);
           }
@@ -244,6 +258,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else {
       // ---------------------------------------------------------- scales: warp 2 + i has rows 64 i .. 64 i + 63
       const int r0 = (warp - 2) * 64 + lane;
+      if (p.early) pdl_wait();
       uint32_t kbg = 0;
       bool ok = true;
       for (int w = blockIdx.x; w < total && ok; w += gridDim.x) {
@@ -300,6 +315,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // single: [128 half, + 128)
     auto load_col = [&](int st) { return DUAL ? (st >> 1) * 128 + half * 64 + (st & 1) * 32 : half * 128 + st * 32; };
     const float2* my_sc = &aux.sc[0][r];
+    if (p.early) pdl_wait();
     uint32_t kbg = 0;
     for (int w = blockIdx.x; w < total; w += gridDim.x) {
       const Item it = decode_item(aux, p.G, w);
@@ -430,13 +446,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_dealloc(tmem_base, TMEM_COLS);
   }
   if (threadIdx.x == 0 && aux.abort) record_status(p.status, MOE_ERR_TIMEOUT);
+  if (p.early) pdl_wait();  // complete only after the launch before
 }
 
 template <bool DUAL>
 cudaError_t launch_typed(const Ctx& c, const Fp8GemmArgs& a) {
   CUtensorMap mA, m0, m1;
   if (!make_maps(a, TILE_ROWS, &mA, &m0, &m1)) return cudaErrorInvalidValue;
-  const Params p = make_params(c, a, a.a_fmt, a.b_fmt, TILE_ROWS);
+  Params p = make_params(c, a, a.a_fmt, a.b_fmt, TILE_ROWS);
+  p.early = a.early;
   const long long tiles = a.rows / TILE_ROWS + std::min(a.G, a.rows);
   const long long items = tiles * (DUAL ? p.n_tiles : (p.n_tiles + 1) / 2);
   auto kern = fp8_rows_gemm_kernel<DUAL>;
