@@ -249,3 +249,31 @@ def test_forward_and_backward_in_a_graph():
         run()
         assert all(torch.equal(a, b) for a, b in zip(got, (ids, w, dl)))
     assert moe.last_device_status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("T,E,K,dtype,pad,groups,kept", [
+    (4096, 256, 20, torch.float32, 0, 1, 1), (2048, 256, 32, torch.bfloat16, 0, 8, 3), (513, 256, 8, torch.bfloat16, 8, 4, 2),
+    (300, 255, 12, torch.float32, 0, 15, 4), (300, 224, 7, torch.float32, 3, 7, 4), (64, 96, 32, torch.float32, 0, 16, 9)])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("biased", [False, True])
+def test_many_candidates(T, E, K, dtype, pad, groups, kept, scoring, biased):
+    """More experts in question than a warp has lanes, rows that are and are not 16-byte aligned, groups of lanes and of
+    odd sizes, and enough tokens that some of their keys are too near to each other for f32."""
+    l, g = _logits(T, E, dtype, pad, T + 5 * E)
+    bias = torch.randn(E, generator=g, device="cuda") * 0.1 if biased else None
+    _check(l, K, bias, scoring=scoring, n_groups=groups, topk_groups=kept, group_score="top2")
+    _check(l, K, bias, scoring=scoring, n_groups=groups, topk_groups=kept, renormalize=False)
+
+
+def test_bias_extremes():
+    """Biases that outweigh the scores, that differ by less than f32 resolves beside them, and a logit's own copies."""
+    T, E, K = 50, 64, 6
+    l, g = _logits(T, E, torch.float32, 0, 21)
+    l = l.clone()
+    l[:, 1::2] = l[:, ::2]
+    for bias in (torch.randn(E, generator=g, device="cuda") * 1e4,
+                 1024.0 + torch.randint(0, 3, (E,), generator=g, device="cuda").float() * 2.0 ** -13,
+                 torch.zeros(E, device="cuda")):
+        for scoring in ("softmax", "sigmoid"):
+            _check(l, K, bias, scoring=scoring)
+            _check(l, K, bias, scoring=scoring, n_groups=8, topk_groups=4, group_score="top2")
