@@ -758,13 +758,17 @@ void set_split(const Ctx& c, Params& p, long long items) {
     }
 }
 
+// Items of a launch, no fewer than there can be.
+long long items_of(const Fp8GemmArgs& a) {
+  return static_cast<long long>(a.rows / NT + std::min(a.G, a.rows)) * ((a.N + WM - 1) / WM);
+}
+
 template <bool DUAL>
 cudaError_t launch_typed(const Ctx& c, const Fp8GemmArgs& a) {
   CUtensorMap mA, m0, m1;
   if (!make_maps(a, a.gather ? 1 : NT, &mA, &m0, &m1)) return cudaErrorInvalidValue;
   Params p = make_params(c, a, a.b_fmt, a.a_fmt, WM);
-  const long long tiles = a.rows / NT + std::min(a.G, a.rows);  // no fewer than there can be
-  const long long items = tiles * p.n_tiles;
+  const long long items = items_of(a);
   p.early = a.early;
   auto kern = fp8_gemm_kernel<DUAL>;
   constexpr size_t smem = kSmem<DUAL>;
@@ -795,7 +799,10 @@ double mean_rows(int rows, int G) { return static_cast<double>(rows) / std::max(
 // Up to how many of them this form is the faster one.  Measured on whole passes of the experts (64 experts of 2816 x 704,
 // 64 of 1024 x 2048, 16 of 2048 x 1024, 128 of 2048 x 768; us here / in fp8_gemm_rows.cu): the dual product with 14 rows a
 // group 89 / 94, 89 / 90, 32 / 37, 124 / 124 (with 20 rows the other one, by 1 to 5 us); the single one with 6 rows
-// 82 / 85, 79 / 81, 34 / 33, 108 / 110, with 10 rows 88 / 88, 82 / 84, 35 / 33, 126 / 123.
+// 82 / 85, 79 / 81, 34 / 33, 108 / 110, with 10 rows 88 / 88, 82 / 84, 35 / 33, 126 / 123.  Whatever the rows, it is also
+// faster while its items do not fill the GPU, since they are smaller and share their k-blocks (one product, 16 x 2048 x
+// 7168: 11 / 26, 200 x 2048 x 7168, 112 items: 22 / 33, 500 x 512 x 2048: 12 / 15; but 500 x 2048 x 7168, 256 items:
+// 38 / 33, 96 x 7168 x 2048, 168 items: 16 / 14).
 constexpr double kSmallRowsDual = 16.0, kSmallRows = 8.0;
 
 }  // namespace
@@ -807,7 +814,7 @@ cudaError_t launch_fp8_gemm(const Ctx& c, const Fp8GemmArgs& a) {
   if (a.G > MAX_G || a.N % 32 || a.K % 32 || a.N <= 0 || a.K <= 0) return cudaErrorInvalidValue;
   const double rows = mean_rows(a.rows, a.G);
   if (a.gather && (!a.dual || rows > kSmallRowsDual)) return cudaErrorInvalidValue;
-  if (rows > (a.dual ? kSmallRowsDual : kSmallRows)) return launch_fp8_rows_gemm(c, a);
+  if (rows > (a.dual ? kSmallRowsDual : kSmallRows) && items_of(a) > c.num_sms) return launch_fp8_rows_gemm(c, a);
   return a.dual ? launch_typed<true>(c, a) : launch_typed<false>(c, a);
 }
 

@@ -666,3 +666,11 @@ def test_quantize_in_a_graph():
         _ok()
         assert torch.equal(got, y)
         _check_product(got, q, s, qw, sw, [0, 11, 40])
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 512, 2080), (160, 256, 1056), (500, 32, 160), (600, 1024, 256), (1000, 544, 96)])
+def test_product_of_one_matrix_by_rows(M, N, K):
+    """From few items, that share k-blocks, to many rows: both forms of the product, on both sides of the crossover."""
+    a, sa, b, sb = _operands(M, 1, N, K, "e4m3", "e5m2", M + N)
+    _check_product(_product(a, sa, b, sb, None, torch.bfloat16), a, sa, b, sb, [0, M])
+    _check_product(_product(a, sa, b, sb, None, torch.float32), a, sa, b, sb, [0, M])
