@@ -450,23 +450,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int n16 = (it.n + 15) & ~15;
       const bool alt = it.n <= 16;  // the halves take k-blocks in turn, both the first 16 columns
       const int col0 = alt ? 0 : half * HALF;
-      if (!DUAL) {  // output row and scale of each column
-        for (int c = et; c < NT; c += EPI_WARPS * 32) {
-          int d = -1;
-          float rs = 1.f;
-          if (c < it.n) {
-            d = p.row_map ? p.row_map[it.row0 + c] : it.row0 + c;
-            if (d < 0 || d >= p.rows) {
-              record_status(p.status, MOE_ERR_DEVICE_INDEX);
-              d = -1;
-            } else if (p.row_scale) {
-              rs = p.row_scale[d];
-            }
-          }
-          aux.dest[parity][c] = d;
-          aux.rscale[parity][c] = rs;
-        }
-      }
+      // single: thread c < NT has column c's output row, first looked at after the k-blocks
+      int d = et < it.n ? it.row0 + et : -1;
+      if (!DUAL && et < it.n && p.row_map) d = p.row_map[it.row0 + et];
       // acc[m][half of the lanes][2 i + b]: columns 8 i + lc, + 1 of row 16 half + 8 b + lr
       unsigned long long acc[MATS][2][2 * X];
 #pragma unroll
@@ -510,6 +496,19 @@ __global__ void __launch_bounds__(THREADS, 1)
           mbar_arrive(&aux.tempty[buf]);
           if (alt) mbar_arrive(&aux.tempty[buf]);  // for the other half's warp
         }
+      }
+      if (!DUAL && et < NT) {
+        float rs = 1.f;
+        if (et < it.n) {
+          if (d < 0 || d >= p.rows) {
+            record_status(p.status, MOE_ERR_DEVICE_INDEX);
+            d = -1;
+          } else if (p.row_scale) {
+            rs = p.row_scale[d];
+          }
+        }
+        aux.dest[parity][et] = d;
+        aux.rscale[parity][et] = rs;
       }
       // uniform over the epilogue: either every warp has all k-blocks or the tile is dropped; also orders dest
       alive = named_barrier_and(1, EPI_WARPS * 32, ok);

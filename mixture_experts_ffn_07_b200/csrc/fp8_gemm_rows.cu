@@ -321,17 +321,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       const Item it = decode_item(aux, p.G, w);
       const int valid = it.n, row_base = it.row0;
       const bool live = q * 32 < valid;  // warp-uniform
-      int dest = -1;  // single: this row's output row and its scale
-      float rs = 1.f;
-      if (!DUAL && r < valid) {
-        dest = p.row_map ? p.row_map[row_base + r] : row_base + r;
-        if (dest < 0 || dest >= p.rows) {
-          record_status(p.status, MOE_ERR_DEVICE_INDEX);
-          dest = -1;
-        } else if (p.row_scale) {
-          rs = p.row_scale[dest];
-        }
-      }
+      // single: this row's output row, first looked at after the k-blocks, so that they do not wait for it
+      int dest = row_base + r;
+      if (!DUAL && r < valid && p.row_map) dest = p.row_map[row_base + r];
       unsigned long long acc[4][16];  // 32 columns each
 #pragma unroll
       for (int st = 0; st < 4; ++st)
@@ -369,6 +361,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       // uniform over the epilogue: either every warp has all k-blocks or the tile is dropped
       if (!named_barrier_and(1, EPI_WARPS * 32, ok)) break;
+      float rs = 1.f;
+      if (!DUAL) {
+        if (r >= valid) {
+          dest = -1;
+        } else if (dest < 0 || dest >= p.rows) {
+          record_status(p.status, MOE_ERR_DEVICE_INDEX);
+          dest = -1;
+        } else if (p.row_scale) {
+          rs = p.row_scale[dest];
+        }
+      }
       if (DUAL) {
         // h = act(g) * u in place of g, its largest value over the row's 128 outputs, codes
         const ActCoef ac = act_coef(p.act);
