@@ -70,9 +70,23 @@ class SelectDesc:
     renormalize: bool = True
     scale: float = 1.0
 
+    def __setattr__(self, name, value):
+        self.__dict__.pop("_refs", None)
+        self.__dict__[name] = value
+
+    def __getstate__(self):
+        return {n: v for n, v in self.__dict__.items() if n != "_refs"}
+
     def c(self, logits_dtype: int) -> _lib.MoeSelectDesc:
         return _lib.MoeSelectDesc(self.T, self.E, self.top_k, GATINGS[self.scoring], self.n_groups, self.topk_groups,
                                   GROUP_SCORES[self.group_score], int(self.renormalize), logits_dtype, self.scale)
+
+    def ref(self, logits_dtype: int):
+        """The C struct by reference, made once until a field is set (small calls take a few microseconds in all)."""
+        refs = self.__dict__.setdefault("_refs", {})
+        if logits_dtype not in refs:
+            refs[logits_dtype] = ctypes.byref(self.c(logits_dtype))
+        return refs[logits_dtype]
 
 
 @dataclass
@@ -210,13 +224,16 @@ def q6_k_srow_bytes(cols: int) -> int:
 class _Types:
     """moe_dtype of each torch dtype that an argument of the calls below may have (made at the first call, so that
     importing the package does not import torch)."""
-    i32 = f32 = act = bf16 = fp8 = torch = None
+    i32 = f32 = act = bf16 = fp8 = torch = current_device = raw_stream = None
 
     @classmethod
     def ready(cls):
         if cls.i32 is None:
             import torch
             cls.torch = torch
+            cls.current_device = torch._C._cuda_getDevice
+            # the raw handle: building a torch.cuda.Stream to read it from takes as long as the launch
+            cls.raw_stream = torch._C._cuda_getCurrentRawStream
             cls.i32 = {torch.int32: 0}
             cls.f32 = {torch.float32: MOE_F32}
             cls.act = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
@@ -240,23 +257,23 @@ def _arg(name, t, types, shape, device=None, dense=True):
     return code
 
 
-def _row_stride(name, t):
-    """Elements between the rows of a 2-D tensor whose rows are dense."""
-    rows, cols = t.shape
+def _row_stride(name, t, cols):
+    """Elements between the rows of a tensor [rows, cols] whose rows are dense."""
+    if t.is_contiguous():
+        return cols or 1
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}: the elements of a row are not consecutive")
-    return t.stride(0) if rows > 1 else max(cols, 1)
+    return t.stride(0) if t.shape[0] > 1 else cols
 
 
-def _call(device, fn, name, *args, stream):
+def _call(device, stream, name, fn, *args):
     """One library call with `device` current, on `stream` (default: that device's current stream)."""
-    torch = _Types.torch
-    if torch._C._cuda_getDevice() != device:
-        with torch.cuda.device(device):
-            return _call(device, fn, name, *args, stream=stream)
-    # the raw handle: building a torch.cuda.Stream to read it from takes as long as the launch
-    raw = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream)
-    code = fn(*args, raw)
+    raw = _Types.raw_stream(device) if stream is None else _stream(stream)
+    if _Types.current_device() == device:
+        code = fn(*args, raw)
+    else:
+        with _Types.torch.cuda.device(device):
+            code = fn(*args, raw)
     if code != MOE_OK:
         raise MoeError(code, name)
 
@@ -267,15 +284,15 @@ def select(desc, logits, ids, w, bias=None, scores=None, stream=None):
     ty = _Types.ready()
     T, E, K = desc.T, desc.E, desc.top_k
     code = _arg("logits", logits, ty.act, (T, E), dense=False)
-    ld, dev = _row_stride("logits", logits), logits.get_device()
+    ld, dev = _row_stride("logits", logits, E), logits.get_device()
     _arg("ids", ids, ty.i32, (T, K), dev)
     _arg("w", w, ty.f32, (T, K), dev)
     if bias is not None:
         _arg("bias", bias, ty.f32, (E,), dev)
     if scores is not None:
         _arg("scores", scores, ty.f32, (T, E), dev)
-    _call(dev, _lib.lib().moe_select, "moe_select", ctypes.byref(desc.c(code)), logits.data_ptr(), ld, _ptr(bias),
-          ids.data_ptr(), w.data_ptr(), _ptr(scores), stream=stream)
+    _call(dev, stream, "moe_select", _lib.lib().moe_select, desc.ref(code), logits.data_ptr(), ld, _ptr(bias),
+          ids.data_ptr(), w.data_ptr(), _ptr(scores))
 
 
 def select_backward(desc, logits, ids, d_w, d_logits, d_scores=None, stream=None):
@@ -283,15 +300,15 @@ def select_backward(desc, logits, ids, d_w, d_logits, d_scores=None, stream=None
     ty = _Types.ready()
     T, E, K = desc.T, desc.E, desc.top_k
     code = _arg("logits", logits, ty.act, (T, E), dense=False)
-    ld, dev = _row_stride("logits", logits), logits.get_device()
+    ld, dev = _row_stride("logits", logits, E), logits.get_device()
     _arg("ids", ids, ty.i32, (T, K), dev)
     _arg("d_w", d_w, ty.f32, (T, K), dev)
     if d_scores is not None:
         _arg("d_scores", d_scores, ty.f32, (T, E), dev)
     if _arg("d_logits", d_logits, ty.act, (T, E), dev) != code:
         raise ValueError(f"d_logits: {d_logits.dtype}, expected {logits.dtype}")
-    _call(dev, _lib.lib().moe_select_backward, "moe_select_backward", ctypes.byref(desc.c(code)), logits.data_ptr(),
-          ld, ids.data_ptr(), d_w.data_ptr(), _ptr(d_scores), d_logits.data_ptr(), stream=stream)
+    _call(dev, stream, "moe_select_backward", _lib.lib().moe_select_backward, desc.ref(code), logits.data_ptr(),
+          ld, ids.data_ptr(), d_w.data_ptr(), _ptr(d_scores), d_logits.data_ptr())
 
 
 def fp8_quantize(x, q, scales, pow2=False, stream=None):
@@ -300,11 +317,11 @@ def fp8_quantize(x, q, scales, pow2=False, stream=None):
     ty = _Types.ready()
     R, C = x.shape
     code = _arg("x", x, ty.act, (R, C), dense=False)
-    ld, dev = _row_stride("x", x), x.get_device()
+    ld, dev = _row_stride("x", x, C), x.get_device()
     fmt = _arg("q", q, ty.fp8, (R, C), dev)
     _arg("scales", scales, ty.f32, ((C + 127) // 128, R), dev)
-    _call(dev, _lib.lib().moe_fp8_quantize, "moe_fp8_quantize", x.data_ptr(), code, R, C, ld, fmt, int(pow2),
-          q.data_ptr(), scales.data_ptr(), stream=stream)
+    _call(dev, stream, "moe_fp8_quantize", _lib.lib().moe_fp8_quantize, x.data_ptr(), code, R, C, ld, fmt, int(pow2),
+          q.data_ptr(), scales.data_ptr())
 
 
 def fp8_quantize_weights(w, q, scales, pow2=False, stream=None):
@@ -318,8 +335,8 @@ def fp8_quantize_weights(w, q, scales, pow2=False, stream=None):
     dev = w.get_device()
     fmt = _arg("q", q, ty.fp8, w.shape, dev)
     _arg("scales", scales, ty.f32, (*G, (N + 127) // 128, (K + 127) // 128), dev)
-    _call(dev, _lib.lib().moe_fp8_quantize_weights, "moe_fp8_quantize_weights", w.data_ptr(), code,
-          G[0] if G else 1, N, K, fmt, int(pow2), q.data_ptr(), scales.data_ptr(), stream=stream)
+    _call(dev, stream, "moe_fp8_quantize_weights", _lib.lib().moe_fp8_quantize_weights, w.data_ptr(), code,
+          G[0] if G else 1, N, K, fmt, int(pow2), q.data_ptr(), scales.data_ptr())
 
 
 def fp8_gemm(a, a_scales, b, b_scales, out, offsets=None, stream=None):
@@ -339,8 +356,8 @@ def fp8_gemm(a, a_scales, b, b_scales, out, offsets=None, stream=None):
     g = G[0] if G else 1
     if offsets is not None:
         _arg("offsets", offsets, ty.i32, (g + 1,), dev)
-    _call(dev, _lib.lib().moe_fp8_gemm, "moe_fp8_gemm", M, N, K, g, a.data_ptr(), a_scales.data_ptr(), af,
-          b.data_ptr(), b_scales.data_ptr(), bf, _ptr(offsets), out.data_ptr(), od, stream=stream)
+    _call(dev, stream, "moe_fp8_gemm", _lib.lib().moe_fp8_gemm, M, N, K, g, a.data_ptr(), a_scales.data_ptr(), af,
+          b.data_ptr(), b_scales.data_ptr(), bf, _ptr(offsets), out.data_ptr(), od)
 
 
 def experts(desc, x, w, topk_ids, topk_w, out, ws, shared_gate=None, stream=None):
@@ -356,9 +373,11 @@ def experts(desc, x, w, topk_ids, topk_w, out, ws, shared_gate=None, stream=None
     _arg("topk_w", topk_w, ty.f32, (T, K), dev)
     if shared_gate is not None:
         _arg("shared_gate", shared_gate, ty.f32, (T,), dev)
-    _call(dev, _lib.lib().moe_experts, "moe_experts", ctypes.byref(desc.c()), x.data_ptr(), ctypes.byref(w.c()),
-          topk_ids.data_ptr(), topk_w.data_ptr(), _ptr(shared_gate), out.data_ptr(), _ptr(ws), _nbytes(ws),
-          stream=stream)
+    for t in (ws, *vars(w).values()):
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"ws or a weight is on {t.device}, not on cuda:{dev}")
+    _call(dev, stream, "moe_experts", _lib.lib().moe_experts, ctypes.byref(desc.c()), x.data_ptr(), ctypes.byref(w.c()),
+          topk_ids.data_ptr(), topk_w.data_ptr(), _ptr(shared_gate), out.data_ptr(), _ptr(ws), _nbytes(ws))
 
 
 def last_device_status(stream=None) -> int:

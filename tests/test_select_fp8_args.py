@@ -1,4 +1,5 @@
 """Argument checks of the selection and 8-bit-float calls, on the host (no device work)."""
+import copy
 import ctypes
 
 import pytest
@@ -144,3 +145,13 @@ def test_tensor_checks():
         moe.fp8_gemm(f(4, 64), f(1, 4), f(64, 64), f(1, 1), f(4, 64))
     with pytest.raises(ValueError):
         moe.experts(moe.Desc(T=4, H=64, E=4, I=64, top_k=2, w_dtype="fp8"), f(4, 64), moe.Weights(), None, None, None, None)
+
+
+def test_select_desc_follows_its_fields():
+    """The struct handed to the library is made again after a field is set, and copies have their own."""
+    d = moe.SelectDesc(T=4, E=8, top_k=2)
+    assert d.ref(0) is d.ref(0) and d.ref(0)._obj.E == 8 and d.ref(1)._obj.logits_dtype == 1
+    other = copy.deepcopy(d)
+    assert other == d
+    d.E, d.scoring = 16, "sigmoid"
+    assert d.ref(0)._obj.E == 16 and d.ref(0)._obj.scoring == d.c(0).scoring and other.ref(0)._obj.E == 8
