@@ -940,8 +940,9 @@ moe_status moe_experts(const moe_desc* d, const void* x, const moe_weights* w, c
   if (d->T == 0) return MOE_OK;
   if ((st = check_expert_weights(*d, w)) != MOE_OK) return st;
   if ((st = check_shared_weights(*d, w)) != MOE_OK) return st;
-  if (!x || !aligned16(x) || !topk_ids || !topk_w || !out || !aligned16(out)) return MOE_ERR_INVALID_ARG;
-  if (shared_gated(*d) && !shared_gate) return MOE_ERR_INVALID_ARG;
+  if (!x || !aligned16(x) || !aligned_scale(topk_ids) || !aligned_scale(topk_w) || !out || !aligned16(out))
+    return MOE_ERR_INVALID_ARG;
+  if (shared_gated(*d) && !aligned_scale(shared_gate)) return MOE_ERR_INVALID_ARG;
   const size_t xb = static_cast<size_t>(d->T) * d->H * (d->act_dtype == MOE_F32 ? 4 : 2);
   const size_t pb = static_cast<size_t>(d->T) * d->top_k * 4;
   if (overlaps(out, xb, x, xb) || overlaps(out, xb, topk_ids, pb) || overlaps(out, xb, topk_w, pb))
@@ -1000,11 +1001,15 @@ moe_status moe_select(const moe_select_desc* d, const void* logits, int64_t stri
                       float* w, float* scores, moe_stream_t stream) {
   const moe_status st = check_select(d, logits, stride);
   if (st != MOE_OK || d->T == 0) return st;
-  if (!ids || !w) return MOE_ERR_INVALID_ARG;
+  if (!aligned_scale(ids) || !aligned_scale(w) || (scores && !aligned_scale(scores))) return MOE_ERR_INVALID_ARG;
   const size_t nl = logits_bytes(*d, stride), np = static_cast<size_t>(d->T) * d->top_k * 4,
                ns = static_cast<size_t>(d->T) * d->E * 4;
   if (overlaps(ids, np, logits, nl) || overlaps(w, np, logits, nl) || overlaps(ids, np, w, np) ||
       (scores && (overlaps(scores, ns, logits, nl) || overlaps(scores, ns, ids, np) || overlaps(scores, ns, w, np))))
+    return MOE_ERR_INVALID_ARG;
+  const size_t nb = static_cast<size_t>(d->E) * 4;
+  if (bias && (!aligned_scale(bias) || overlaps(bias, nb, ids, np) || overlaps(bias, nb, w, np) ||
+               (scores && overlaps(bias, nb, scores, ns))))
     return MOE_ERR_INVALID_ARG;
   moe::Ctx c;
   if (!make_ctx(reinterpret_cast<cudaStream_t>(stream), &c)) return MOE_ERR_CUDA;
@@ -1015,7 +1020,8 @@ moe_status moe_select_backward(const moe_select_desc* d, const void* logits, int
                                const float* d_w, const float* d_scores, void* d_logits, moe_stream_t stream) {
   const moe_status st = check_select(d, logits, stride);
   if (st != MOE_OK || d->T == 0) return st;
-  if (!ids || !d_w || !d_logits) return MOE_ERR_INVALID_ARG;
+  if (!aligned_scale(ids) || !aligned_scale(d_w) || (d_scores && !aligned_scale(d_scores)) || !d_logits)
+    return MOE_ERR_INVALID_ARG;
   const size_t eb = d->logits_dtype == MOE_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(d_logits) % eb) return MOE_ERR_INVALID_ARG;
   const size_t nl = logits_bytes(*d, stride), np = static_cast<size_t>(d->T) * d->top_k * 4,
@@ -1073,12 +1079,13 @@ moe_status moe_fp8_gemm(int64_t M, int64_t N, int64_t K, int64_t G, const void* 
     return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
   if (!a || !b || !out || !aligned16(a) || !aligned16(b) || !aligned16(out) || !aligned_scale(a_scales) ||
-      !aligned_scale(b_scales))
+      !aligned_scale(b_scales) || (offsets && !aligned_scale(offsets)))
     return MOE_ERR_INVALID_ARG;
   const size_t no = static_cast<size_t>(M) * N * (out_dtype == MOE_F32 ? 4 : 2);
   const size_t nkb = (K + 127) / 128;
   if (overlaps(out, no, a, static_cast<size_t>(M) * K) || overlaps(out, no, b, static_cast<size_t>(G) * N * K) ||
-      overlaps(out, no, a_scales, nkb * M * 4) || overlaps(out, no, b_scales, nkb * G * ((N + 127) / 128) * 4))
+      overlaps(out, no, a_scales, nkb * M * 4) || overlaps(out, no, b_scales, nkb * G * ((N + 127) / 128) * 4) ||
+      (offsets && overlaps(out, no, offsets, (G + 1) * 4)))
     return MOE_ERR_INVALID_ARG;
   moe::Ctx c;
   if (!make_ctx(reinterpret_cast<cudaStream_t>(stream), &c)) return MOE_ERR_CUDA;

@@ -155,3 +155,19 @@ def test_select_desc_follows_its_fields():
     assert other == d
     d.E, d.scoring = 16, "sigmoid"
     assert d.ref(0)._obj.E == 16 and d.ref(0)._obj.scoring == d.c(0).scoring and other.ref(0)._obj.E == 8
+
+
+def test_every_pointer_is_aligned_and_apart():
+    L = _lib.lib()
+    e4, f32 = _lib.MOE_E4M3, _lib.MOE_F32
+    assert L.moe_select(_sel(), A, 16, B + 1, C, D, None, None) == INV         # bias
+    assert L.moe_select(_sel(), A, 16, C + 16, C, D, None, None) == INV        # bias over ids
+    assert L.moe_select(_sel(), A, 16, None, C + 2, D, None, None) == INV
+    assert L.moe_select(_sel(), A, 16, None, C, D + 2, None, None) == INV
+    assert L.moe_select(_sel(), A, 16, None, C, D, B + 2, None) == INV
+    assert L.moe_select_backward(_sel(), A, 16, B + 2, C, None, D, None) == INV
+    assert L.moe_select_backward(_sel(), A, 16, B, C + 2, None, D, None) == INV
+    assert L.moe_select_backward(_sel(), A, 16, B, C, E_ + 2, D, None) == INV
+    F = 7 << 28
+    assert L.moe_fp8_gemm(4, 64, 64, 2, A, B, e4, C, D, e4, F + 2, E_, f32, None) == INV
+    assert L.moe_fp8_gemm(4, 64, 64, 2, A, B, e4, C, D, e4, E_ + 16, E_, f32, None) == INV  # offsets inside the output
