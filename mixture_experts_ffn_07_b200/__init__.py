@@ -344,16 +344,17 @@ def fp8_gemm(a, a_scales, b, b_scales, out, offsets=None, stream=None):
     [G, ceil(N/128), ceil(K/128)] (or without G) -> out [M,N] (f32 or bf16); offsets [G+1] int32 groups the rows."""
     ty = _Types.ready()
     M, K = a.shape
-    *G, N, _ = b.shape
-    if len(G) > 1:
+    shape = b.shape
+    if len(shape) not in (2, 3):
         raise ValueError("b: [G, N, K] or [N, K] expected")
+    N, kb, dev = shape[-2], (K + 127) // 128, a.get_device()
+    stack = len(shape) == 3
+    g = shape[0] if stack else 1
     af = _arg("a", a, ty.fp8, (M, K))
-    dev, kb = a.get_device(), (K + 127) // 128
-    bf = _arg("b", b, ty.fp8, (*G, N, K), dev)
+    bf = _arg("b", b, ty.fp8, (g, N, K) if stack else (N, K), dev)
     _arg("a_scales", a_scales, ty.f32, (kb, M), dev)
-    _arg("b_scales", b_scales, ty.f32, (*G, (N + 127) // 128, kb), dev)
+    _arg("b_scales", b_scales, ty.f32, (g, (N + 127) // 128, kb) if stack else ((N + 127) // 128, kb), dev)
     od = _arg("out", out, ty.act, (M, N), dev)
-    g = G[0] if G else 1
     if offsets is not None:
         _arg("offsets", offsets, ty.i32, (g + 1,), dev)
     _call(dev, stream, "moe_fp8_gemm", _lib.lib().moe_fp8_gemm, M, N, K, g, a.data_ptr(), a_scales.data_ptr(), af,

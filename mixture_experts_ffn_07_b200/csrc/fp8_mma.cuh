@@ -170,8 +170,11 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t groups, uint64_t rows, 
 // Tensor maps of the rows (boxes of a_box) and of one or two weight stacks (boxes of 128 rows).
 bool make_maps(const Fp8GemmArgs& a, uint32_t a_box, CUtensorMap* mA, CUtensorMap* m0, CUtensorMap* m1) {
   const uint64_t G = a.G, N = a.N, K = a.K;
-  return make_map(mA, a.A, 0, static_cast<uint64_t>(a.gather ? a.a_ld : a.rows), K, a_box) && make_map(m0, a.B0, G, N, K, WM) &&
-         make_map(m1, a.dual ? a.B1 : a.B0, G, N, K, WM);
+  if (!make_map(mA, a.A, 0, static_cast<uint64_t>(a.gather ? a.a_ld : a.rows), K, a_box) || !make_map(m0, a.B0, G, N, K, WM))
+    return false;
+  if (a.dual) return make_map(m1, a.B1, G, N, K, WM);
+  *m1 = *m0;  // not read
+  return true;
 }
 
 // `m_fmt`, `n_fmt`: formats of the MMA's M and N operands; M its rows (N is set per tile by the kernel).
