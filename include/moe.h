@@ -151,8 +151,10 @@ const char* moe_version(void);
  * T for fixed sizes, plus the bf16 router's split-K partial logits (at most
  * 20480*E*4 bytes) and 256*E*4 bytes of per-CTA expert counts for T > 64, or
  * for 1 <= T <= 64 on the streaming path the fused decode kernel's per-chunk
- * partial logits (ceil(H/1024)*T*(E+1)*4 bytes), in 256-byte aligned regions.  Returns 0 for an invalid
- * descriptor.  moe_route, moe_expert_ffn and moe_combine need no more than this.
+ * partial logits (ceil(H/1024)*T*(E+1)*4 bytes), in 256-byte aligned regions.  With w_dtype MOE_FP8 also
+ * the codes and scales of x and of the hidden rows (about T*H*(1+top_k) + T*top_k*I bytes and 1/32 of that).
+ * Returns 0 for an invalid descriptor.  moe_route, moe_expert_ffn, moe_combine and moe_experts need no more
+ * than this.
  */
 size_t moe_workspace_bytes(const moe_desc* d);
 

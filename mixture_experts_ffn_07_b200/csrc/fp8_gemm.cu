@@ -25,6 +25,8 @@
 //
 // Few items (one decoded token: experts x weight tiles, fewer than SMs) split K over a cluster of up to eight CTAs:
 // each sums its k-blocks, leaves the sums in its shared memory, and the first CTA adds them in rank order.
+// What bounds it: HBM with many experts touched (16 tokens, 128 experts of 2816 x 704: 490 MB in 80 us, 0.95 of the copy
+// rate), latency with few (16 x 2048 x 7168: 11 us, 2.3 of them for its 15 MB).
 // Every wait is bounded; on expiry the CTA records MOE_ERR_TIMEOUT, drains and exits.
 #include <atomic>
 
