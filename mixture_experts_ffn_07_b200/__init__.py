@@ -224,7 +224,7 @@ def q6_k_srow_bytes(cols: int) -> int:
 class _Types:
     """moe_dtype of each torch dtype that an argument of the calls below may have (made at the first call, so that
     importing the package does not import torch)."""
-    i32 = f32 = act = bf16 = fp8 = torch = current_device = raw_stream = None
+    i32 = f32 = act = bf16 = fp8 = e4m3 = torch = current_device = raw_stream = None
 
     @classmethod
     def ready(cls):
@@ -238,6 +238,7 @@ class _Types:
             cls.f32 = {torch.float32: MOE_F32}
             cls.act = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
             cls.bf16 = {torch.bfloat16: MOE_BF16}
+            cls.e4m3 = {torch.float8_e4m3fn: MOE_E4M3}
             cls.fp8 = {torch.float8_e4m3fn: MOE_E4M3, torch.float8_e5m2: MOE_E5M2}
         return cls
 
@@ -361,6 +362,23 @@ def fp8_gemm(a, a_scales, b, b_scales, out, offsets=None, stream=None):
           b.data_ptr(), b_scales.data_ptr(), bf, _ptr(offsets), out.data_ptr(), od)
 
 
+def _fp8_weights(ty, dev, E, H, I, gate, gate_scale, up, up_scale, down, down_scale):
+    """Checks stacks of E experts (None: one matrix each) and their scales."""
+    h, i = (H + 127) // 128, (I + 127) // 128
+    wide, tall, a, b = (I, H), (H, I), (i, h), (h, i)
+    if E is not None:
+        wide, tall, a, b = (E, *wide), (E, *tall), (E, *a), (E, *b)
+    for t in (gate, gate_scale, up, up_scale, down, down_scale):
+        if t is None:
+            raise ValueError("fp8 weights: gate, up and down with their scales are needed")
+    _arg("gate", gate, ty.e4m3, wide, dev)
+    _arg("up", up, ty.e4m3, wide, dev)
+    _arg("down", down, ty.e4m3, tall, dev)
+    _arg("gate_scale", gate_scale, ty.f32, a, dev)
+    _arg("up_scale", up_scale, ty.f32, a, dev)
+    _arg("down_scale", down_scale, ty.f32, b, dev)
+
+
 def experts(desc, x, w, topk_ids, topk_w, out, ws, shared_gate=None, stream=None):
     """moe_experts: the layer on a given routing (topk_ids [T,K] int32, topk_w [T,K] f32): permutation, experts,
     shared expert, combine."""
@@ -374,9 +392,13 @@ def experts(desc, x, w, topk_ids, topk_w, out, ws, shared_gate=None, stream=None
     _arg("topk_w", topk_w, ty.f32, (T, K), dev)
     if shared_gate is not None:
         _arg("shared_gate", shared_gate, ty.f32, (T,), dev)
-    for t in (ws, *vars(w).values()):
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"ws or a weight is on {t.device}, not on cuda:{dev}")
+    if ws is not None and ws.get_device() != dev:
+        raise ValueError(f"ws is on {ws.device}, not on cuda:{dev}")
+    if desc.w_dtype == "fp8":
+        _fp8_weights(ty, dev, desc.E, H, desc.I, w.gate, w.gate_scale, w.up, w.up_scale, w.down, w.down_scale)
+        if desc.shared_I > 0:
+            _fp8_weights(ty, dev, None, H, desc.shared_I, w.sh_gate, w.sh_gate_scale, w.sh_up, w.sh_up_scale, w.sh_down,
+                         w.sh_down_scale)
     _call(dev, stream, "moe_experts", _lib.lib().moe_experts, ctypes.byref(desc.c()), x.data_ptr(), ctypes.byref(w.c()),
           topk_ids.data_ptr(), topk_w.data_ptr(), _ptr(shared_gate), out.data_ptr(), _ptr(ws), _nbytes(ws))
 

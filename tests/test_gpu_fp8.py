@@ -674,3 +674,27 @@ def test_product_of_one_matrix_by_rows(M, N, K):
     a, sa, b, sb = _operands(M, 1, N, K, "e4m3", "e5m2", M + N)
     _check_product(_product(a, sa, b, sb, None, torch.bfloat16), a, sa, b, sb, [0, M])
     _check_product(_product(a, sa, b, sb, None, torch.float32), a, sa, b, sb, [0, M])
+
+
+def test_weights_are_checked():
+    """Stacks and scales of another size, type or layout are refused before anything is launched."""
+    T, H, E, I, K = 8, 256, 4, 160, 2
+    t = _fp8_weights(E, H, I, 64, 95)
+    g = _gen(96)
+    x = torch.randn((T, H), generator=g, device="cuda").to(torch.bfloat16)
+    ids = torch.rand((T, E), generator=g, device="cuda").topk(K, 1).indices.to(torch.int32)
+    tw = torch.rand((T, K), generator=g, device="cuda")
+    d = moe.Desc(T=T, H=H, E=E, I=I, top_k=K, w_dtype="fp8", shared_I=64)
+    launched = moe.launch_count()
+    bad = [dict(gate=t["gate"][:3]), dict(up=t["up"].view(torch.uint8)), dict(down=t["up"]),
+           dict(gate_scale=t["gate_scale"][:, :1].contiguous()), dict(up_scale=t["up_scale"].double()), dict(down_scale=None),
+           dict(gate=t["gate"].view(torch.uint8).transpose(1, 2).contiguous().transpose(1, 2).view(torch.float8_e4m3fn)),
+           dict(sh_down=t["sh_down"][:, :32].contiguous()), dict(sh_gate=None), dict(up=t["up"].cpu())]
+    for b in bad:
+        with pytest.raises(ValueError):
+            _experts(d, x, {**t, **b}, ids, tw)
+    with pytest.raises(ValueError):
+        _experts(d, x, t, ids, tw, ws=torch.empty(moe.workspace_bytes(d), dtype=torch.uint8))
+    assert moe.launch_count() == launched
+    _experts(d, x, t, ids, tw)
+    _ok()
