@@ -698,3 +698,10 @@ def test_weights_are_checked():
     assert moe.launch_count() == launched
     _experts(d, x, t, ids, tw)
     _ok()
+
+
+@pytest.mark.parametrize("shape", [(100, 256, 60, 96, 6, 0), (20, 128, 40, 64, 32, 32), (70, 128, 33, 32, 17, 0), (900, 1056, 5, 96, 5, 0)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_experts_of_many_slots(shape, dtype):
+    """Up to 32 experts a token, and batches past the single front launch whose rows are gathered or put in order."""
+    test_experts(shape, "silu", dtype)
