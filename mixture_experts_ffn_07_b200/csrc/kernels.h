@@ -199,10 +199,11 @@ cudaError_t launch_select_backward(const Ctx& c, const void* logits, int logits_
 
 // Block-scaled 8-bit floats (fp8_quant.cu): rows -> codes [R, C] and scales [ceil(C/128), R]; weight stacks ->
 // codes [G, N, K] and scales [G, ceil(N/128), ceil(K/128)].
+// early: the launch before this one on the stream is a permutation, and x was complete before it.
 cudaError_t launch_fp8_rows(const Ctx& c, const void* x, int x_dtype, int64_t stride, int64_t R, int C, int fmt,
-                            bool pow2, void* q, float* scales);
-// Rows of x coded (e4m3) straight into expert order: row t's codes at rows pair_pos[t*K + k] of x_perm for the pairs with
-// an id in [0, E), and at row t of q unless that is nullptr.
+                            bool pow2, void* q, float* scales, bool early = false);
+// Behind a permutation, with x complete before it: rows of x coded (e4m3) straight into expert order: row t's codes at
+// rows pair_pos[t*K + k] of x_perm for the pairs with an id in [0, E), and at row t of q unless that is nullptr.
 cudaError_t launch_fp8_scatter(const Ctx& c, const void* x, int x_dtype, int R, int C, void* q, float* scales,
                                const int32_t* ids, const int32_t* pair_pos, int K, int E, void* x_perm);
 // Coding of dense rows and the permutation of launch_permute in one launch, for small batches.

@@ -269,14 +269,15 @@ moe_status route_impl(const moe::Ctx& c, const moe_desc& d, const void* x, const
 }
 
 // x as e4m3 codes and scales in the workspace.
-moe_status fp8_code_x(const moe::Ctx& c, const moe_desc& d, const void* x, void* ws, const Layout& L) {
+moe_status fp8_code_x(const moe::Ctx& c, const moe_desc& d, const void* x, void* ws, const Layout& L,
+                      bool early = false) {
   MOE_TRY(moe::launch_fp8_rows(c, x, d.act_dtype, d.H, d.T, d.H, MOE_E4M3, false, at<void>(ws, L.x_q),
-                               at<float>(ws, L.x_qs)));
+                               at<float>(ws, L.x_qs), early));
   return MOE_OK;
 }
 
-// Routed experts on 8-bit floats; x is coded already (in_order: in the workspace's x_perm, in expert order).  tw: slot rows in f32 times the routing weight
-// (moe_expert_ffn); without it slot rows in act_dtype for launch_combine_ids.
+// Routed experts on 8-bit floats; x is coded already (in_order: in the workspace's x_perm, in expert order).  tw: slot
+// rows in f32 times the routing weight (moe_expert_ffn); without it slot rows in act_dtype for launch_combine_ids.
 moe_status fp8_experts(const moe::Ctx& c, const moe_desc& d, const moe_weights& w, const int32_t* offsets,
                        const int32_t* sorted_pairs, const float* tw, void* y_slots, void* ws, const Layout& L,
                        bool in_order = false) {
@@ -531,7 +532,7 @@ moe_status experts_impl(const moe::Ctx& c, const moe_desc& d, const void* x, con
                                       at<float>(ws, L.x_qs), ids, at<int32_t>(ws, L.pair_pos), d.top_k, d.E,
                                       at<void>(ws, L.x_perm)));
     else if (!front)
-      st = fp8_code_x(c, d, x, ws, L);
+      st = fp8_code_x(c, d, x, ws, L, true);
     if (st != MOE_OK) return st;
     st = fp8_experts(c, d, w, offsets, sorted_pairs, nullptr, y_slots, ws, L, scatter);
   } else {

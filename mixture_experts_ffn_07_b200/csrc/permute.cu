@@ -35,9 +35,9 @@ __global__ void __launch_bounds__(kWarps * 32) permute_kernel(const int32_t* __r
   __shared__ int tot[kMaxE];
   __shared__ int excl[kMaxE + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_trigger();
   for (int i = threadIdx.x; i < kWarps * kMaxE; i += blockDim.x) (&hist[0][0])[i] = 0;
   pdl_wait();
+  pdl_trigger();  // after the wait: the coding of x behind it relies on what came before being complete
   __syncthreads();
 
   const int seg = (P + kWarps - 1) / kWarps;
@@ -155,9 +155,9 @@ __global__ void __launch_bounds__(kWarps * 32) permute_cluster_kernel(const int3
   const int rank = static_cast<int>(cluster.block_rank());
   const int ncta = static_cast<int>(cluster.num_blocks());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_trigger();
   for (int i = threadIdx.x; i < kWarps * kMaxE; i += blockDim.x) (&hist[0][0])[i] = 0;
   pdl_wait();
+  pdl_trigger();  // after the wait: the coding of x behind it relies on what came before being complete
   const int base = (rank * kWarps + warp) * 32 * kPerThread;
   int e[kPerThread];
 #pragma unroll

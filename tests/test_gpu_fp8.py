@@ -705,3 +705,31 @@ def test_weights_are_checked():
 def test_experts_of_many_slots(shape, dtype):
     """Up to 32 experts a token, and batches past the single front launch whose rows are gathered or put in order."""
     test_experts(shape, "silu", dtype)
+
+
+@pytest.mark.parametrize("T,H,E", [(12, 512, 16), (100, 512, 64), (400, 512, 8)])
+def test_inputs_written_just_before(T, H, E):
+    """x, ids and weights come from launches right before the call, on its stream, and change from call to call."""
+    I, K = 128, 4
+    t = _fp8_weights(E, H, I, 0, 97)
+    d = moe.Desc(T=T, H=H, E=E, I=I, top_k=K, w_dtype="fp8")
+    w, ws = moe.Weights(**t), torch.empty(moe.workspace_bytes(d), dtype=torch.uint8, device="cuda")
+    g = _gen(98)
+    xs = torch.randn((6, T, H), generator=g, device="cuda").to(torch.bfloat16)
+    idss = torch.rand((6, T, E), generator=g, device="cuda").topk(K, 2).indices.to(torch.int32)
+    tws = torch.rand((6, T, K), generator=g, device="cuda")
+    want = [_experts(d, xs[i], t, idss[i], tws[i]) for i in range(6)]
+    _ok()
+    x, ids, tw = torch.empty_like(xs[0]), torch.empty_like(idss[0]), torch.empty_like(tws[0])
+    slow = torch.randn((4096, 4096), device="cuda")
+    outs = torch.empty((60, T, H), dtype=torch.bfloat16, device="cuda")
+    for i in range(60):
+        if i % 7 == 0:
+            slow = torch.mm(slow, slow) * 1e-4  # a launch that takes longer than the call
+        tw.copy_(tws[i % 6])
+        ids.copy_(idss[i % 6])
+        x.copy_(xs[i % 6])
+        moe.experts(d, x, w, ids, tw, outs[i], ws)
+    _ok()
+    for i in range(60):
+        assert torch.equal(outs[i], want[i % 6]), i
