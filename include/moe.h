@@ -450,8 +450,9 @@ moe_status moe_fp8_gemm(int64_t M, int64_t N, int64_t K, int64_t G, const void* 
  * appear twice in a token's ids.
  *  topk_ids [T,K] int32, topk_w [T,K] f32; shared_gate [T] f32 (required iff shared_I > 0 and has_shared_gate,
  *  else ignored); x, out, w, ws as for moe_layer (w->router and the routing fields of d are not used).
- * The MOE_FP8 slot rows are kept in act_dtype (bf16 slots as in moe_layer's
- * tensor-core path) and added in slot order in f32.
+ * The MOE_FP8 slot rows are kept in f32, or, in large batches of bf16 layers, in
+ * f16 with a power of two for each 128 outputs of a row (11 significant bits);
+ * they are added in slot order in f32, and a bf16 output is rounded once.
  */
 moe_status moe_experts(const moe_desc* d, const void* x, const moe_weights* w, const int32_t* topk_ids,
                        const float* topk_w, const float* shared_gate, void* out, void* ws, size_t ws_bytes,

@@ -760,8 +760,8 @@ void set_split(const Ctx& c, Params& p, long long items) {
 }
 
 // Items of a launch, no fewer than there can be.
-long long items_of(const Fp8GemmArgs& a) {
-  return static_cast<long long>(a.rows / NT + std::min(a.G, a.rows)) * ((a.N + WM - 1) / WM);
+long long items_of(int rows, int N, int G) {
+  return static_cast<long long>(rows / NT + std::min(G, rows)) * ((N + WM - 1) / WM);
 }
 
 template <bool DUAL>
@@ -769,7 +769,7 @@ cudaError_t launch_typed(const Ctx& c, const Fp8GemmArgs& a) {
   CUtensorMap mA, m0, m1;
   if (!make_maps(a, a.gather ? 1 : NT, &mA, &m0, &m1)) return cudaErrorInvalidValue;
   Params p = make_params(c, a, a.b_fmt, a.a_fmt, WM);
-  const long long items = items_of(a);
+  const long long items = items_of(a.rows, a.N, a.G);
   p.early = a.early;
   auto kern = fp8_gemm_kernel<DUAL>;
   constexpr size_t smem = kSmem<DUAL>;
@@ -808,14 +808,19 @@ constexpr double kSmallRowsDual = 16.0, kSmallRows = 8.0;
 
 }  // namespace
 
+bool fp8_gemm_many(int num_sms, int rows, int N, int G, bool dual) {
+  return mean_rows(rows, G) > (dual ? kSmallRowsDual : kSmallRows) && items_of(rows, N, G) > std::min(num_sms, kFp8MaxSms);
+}
+
 bool fp8_gemm_gathers(int rows, int G) { return mean_rows(rows, G) <= kSmallRowsDual; }
 
 cudaError_t launch_fp8_gemm(const Ctx& c, const Fp8GemmArgs& a) {
   if (a.rows <= 0 || a.G <= 0) return cudaSuccess;
   if (a.G > MAX_G || a.N % 32 || a.K % 32 || a.N <= 0 || a.K <= 0) return cudaErrorInvalidValue;
-  const double rows = mean_rows(a.rows, a.G);
-  if (a.gather && (!a.dual || rows > kSmallRowsDual)) return cudaErrorInvalidValue;
-  if (rows > (a.dual ? kSmallRowsDual : kSmallRows) && items_of(a) > c.num_sms) return launch_fp8_rows_gemm(c, a);
+  if (a.gather && (!a.dual || mean_rows(a.rows, a.G) > kSmallRowsDual)) return cudaErrorInvalidValue;
+  const bool many = fp8_gemm_many(c.num_sms, a.rows, a.N, a.G, a.dual);
+  if (a.out_f16 && (!many || a.dual || a.a_fmt != MOE_E4M3 || a.b_fmt != MOE_E4M3 || a.row_scale)) return cudaErrorInvalidValue;
+  if (many) return launch_fp8_rows_gemm(c, a);
   return a.dual ? launch_typed<true>(c, a) : launch_typed<false>(c, a);
 }
 

@@ -99,6 +99,22 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// The power of two that brings 128 outputs of a row into f16, and its inverse, from the sum of their k-blocks' |scale|:
+// a block of 128 products of two e4m3 codes is at most 128 * 448^2 in size, so the outputs are below `top`, and
+// 2^e > top brings them below 2^15 (f32 roundings on the way are far from the factor 2 that is left).  The values lie a
+// few hundred times below the bound, where f16 has 11 significant bits down to 2^-29 of it: 2^-11 relative, 8 times
+// finer than bf16 rows, for the same bytes.
+__device__ __forceinline__ float f16_scale(float scales, float& back) {
+  const float top = fminf(scales * (128.f * 448.f * 448.f), 3.4028235e38f);  // (a NaN counts as the largest)
+  const int e = max(static_cast<int>(__float_as_uint(top) >> 23) - 126, -110);
+  back = __uint_as_float(static_cast<uint32_t>(127 + e - 15) << 23);
+  return __uint_as_float(static_cast<uint32_t>(127 + 15 - e) << 23);
+}
+
 __device__ __forceinline__ uint4 f32x4(float a, float b, float c, float d) {
   return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
 }
@@ -333,6 +349,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int st = 0; st < 4; ++st)
 #pragma unroll
         for (int j = 0; j < 16; ++j) acc[st][j] = 0ull;
+      float scales = 0.f;  // single: sum of the k-blocks' |scale|
       bool ok = true;
       for (int kb = 0; kb < nkb; ++kb, ++kbg) {
         const int buf = kbg % NBUF;
@@ -345,6 +362,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const float2 f = my_sc[(kbg % SLOTS) * TILE_ROWS];  // written before the MMA was issued
           const unsigned long long s0 = DUAL ? join2(f.x, f.x) : (half ? join2(f.y, f.y) : join2(f.x, f.x));
           const unsigned long long s1 = DUAL ? join2(f.y, f.y) : s0;
+          if (!DUAL) scales += fabsf(half ? f.y : f.x);
           // 16 columns at a time and one load in flight: the other warp of the scheduler fills the wait, and no
           // accumulator spills (two loads of 16 in flight, or one of 32 consecutive registers, spilled a few registers
           // in this loop and cost a fifth of the time)
@@ -415,6 +433,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       } else if (dest >= 0) {
         const int col = (2 * it.wt + half) * WM;
+        if (p.out_f16) {
+          float back;
+          rs = f16_scale(scales, back);
+          if (col < p.N) p.out_f16_scale[static_cast<long long>(dest) * p.n_tiles + 2 * it.wt + half] = back;
+        }
 #pragma unroll
         for (int st = 0; st < 4; ++st) {
           if (col + 32 * st >= p.N) break;
@@ -428,7 +451,13 @@ __global__ void __launch_bounds__(THREADS, 1)
               y[2 * j] *= rs;
               y[2 * j + 1] *= rs;
             }
-            if (p.out_bf16) {
+            if (p.out_f16) {
+              store32(p.out_f16 + at + 16 * h,
+                      make_uint4(f16_pair(y[0], y[1]), f16_pair(y[2], y[3]), f16_pair(y[4], y[5]), f16_pair(y[6], y[7])),
+                      make_uint4(f16_pair(y[8], y[9]), f16_pair(y[10], y[11]), f16_pair(y[12], y[13]),
+                                 f16_pair(y[14], y[15])),
+                      p.wide);
+            } else if (p.out_bf16) {
               store32(p.out_bf16 + at + 16 * h,
                       make_uint4(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]), bf16_pair(y[4], y[5]), bf16_pair(y[6], y[7])),
                       make_uint4(bf16_pair(y[8], y[9]), bf16_pair(y[10], y[11]), bf16_pair(y[12], y[13]),

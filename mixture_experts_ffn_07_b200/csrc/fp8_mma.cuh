@@ -34,6 +34,8 @@ struct Params {
   float* out_qs;                // [ceil(N/128), rows]
   float* out_f32;
   __nv_bfloat16* out_bf16;
+  __half* out_f16;              // with out_f16_scale [rows, n_tiles]: kSlotsF16
+  float* out_f16_scale;
   const int32_t* row_map;
   const float* row_scale;
   bool wide;                    // outputs allow 32-byte stores
@@ -203,9 +205,12 @@ Params make_params(const Ctx& c, const Fp8GemmArgs& a, int m_fmt, int n_fmt, int
   p.out_qs = a.out_qs;
   p.out_f32 = a.out_f32;
   p.out_bf16 = a.out_bf16;
+  p.out_f16 = a.out_f16;
+  p.out_f16_scale = a.out_f16_scale;
   p.row_map = a.row_map;
   p.row_scale = a.row_scale;
-  const void* out = a.dual ? a.out_q : a.out_bf16 ? static_cast<const void*>(a.out_bf16) : a.out_f32;
+  const void* out = a.dual ? a.out_q : a.out_bf16 ? static_cast<const void*>(a.out_bf16)
+                    : a.out_f16 ? static_cast<const void*>(a.out_f16) : a.out_f32;
   p.wide = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   p.status = c.status;
   p.wait_limit = c.wait_limit;

@@ -1,5 +1,7 @@
 // Quantisation to block-scaled 8-bit floats (fp8.cuh): activation rows with one scale per 128 values, weight
 // matrices with one scale per 128 x 128 block, and the combine of the 8-bit experts' slot rows.
+#include <type_traits>
+
 #include "fp8.cuh"
 
 namespace moe {
@@ -318,6 +320,19 @@ struct Slots<__nv_bfloat16> {
     }
   }
 };
+template <>
+struct Slots<__half> {  // kSlotsF16, without the power of two
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void values(const uint4& r, float (&v)[N]) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+};
 template <int N>
 __device__ __forceinline__ void store_row(float* p, const float (&v)[N]) {
 #pragma unroll
@@ -338,30 +353,55 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&v)[N])
 // out[t] = sum_k w[t,k] y[t*K+k] in slot order in f32 (w == nullptr: 1; slots whose expert id is outside [0, E)
 // hold no row and count nothing), + y_shared[t].  A CTA has one token and 256 threads' worth of its outputs, 16 bytes
 // of each slot row a thread; the rows are loaded beside the ids and weights, not after them (one of no expert is
-// memory that nobody wrote, and is dropped).
+// memory that nobody wrote, and is dropped).  Of f16 rows the powers of two are asked for before the rows, each by one
+// thread of the CTA, and multiplied into the weight: asked for after them, and into every value, 8192 tokens of 7168 with
+// 8 slots took 285 us, this takes 220 (bf16 rows, without them, 188).
 constexpr int kCombineThreads = 256;
 template <typename T, typename OT>
 __global__ void __launch_bounds__(kCombineThreads)
     combine_ids_kernel(const T* __restrict__ y, const float* __restrict__ w, const int32_t* __restrict__ ids,
                        const float* __restrict__ y_shared, int K, int E, int H, OT* __restrict__ out) {
   constexpr int N = Slots<T>::N;
+  constexpr bool kScaled = std::is_same<T, __half>::value;
+  constexpr int kAcross = kCombineThreads * N / kFp8Block;  // blocks of 128 outputs
   __shared__ float weight[kMaxSlots];
   __shared__ int valid[kMaxSlots];
+  __shared__ float scale[kScaled ? kMaxSlots : 1][kAcross];
   const long long t = blockIdx.x;
   const int c = (blockIdx.y * kCombineThreads + threadIdx.x) * N;
   const bool in = c < H;
   pdl_trigger();
   pdl_wait();
   const T* row = y + t * K * H + (in ? c : 0);
+  float s[2] = {0.f, 0.f}, my_w = 1.f;
+  int id = -1;
+  if (threadIdx.x < K) {
+    id = ids[t * K + threadIdx.x];
+    if (w) my_w = w[t * K + threadIdx.x];
+  }
+  const int blocks = (H + kFp8Block - 1) / kFp8Block;
+  if (kScaled) {  // the powers of two of the CTA's columns
+    const float* from = reinterpret_cast<const float*>(y + static_cast<long long>(gridDim.x) * K * H) + t * K * blocks;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = threadIdx.x + j * kCombineThreads, b = blockIdx.y * kAcross + i % kAcross;
+      if (i < K * kAcross && b < blocks) s[j] = __ldg(from + i / kAcross * blocks + b);
+    }
+  }
   uint4 r[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
     if (j < K) r[j] = __ldg(reinterpret_cast<const uint4*>(row + static_cast<long long>(j) * H));
   if (threadIdx.x < K) {
-    const int id = ids[t * K + threadIdx.x];
     valid[threadIdx.x] = id >= 0 && id < E;
-    weight[threadIdx.x] = w ? w[t * K + threadIdx.x] : 1.f;
+    weight[threadIdx.x] = my_w;
   }
+  if (kScaled)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int i = threadIdx.x + j * kCombineThreads;
+      if (i < K * kAcross) scale[i / kAcross][i % kAcross] = s[j];
+    }
   float acc[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) acc[i] = 0.f;
@@ -377,7 +417,7 @@ __global__ void __launch_bounds__(kCombineThreads)
       if (k0 + j < K && valid[k0 + j]) {
         float v[N];
         Slots<T>::values(r[j], v);
-        const float ww = weight[k0 + j];
+        const float ww = kScaled ? weight[k0 + j] * scale[k0 + j][threadIdx.x * N / kFp8Block] : weight[k0 + j];
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] += ww * v[i];
       }
@@ -473,6 +513,7 @@ cudaError_t launch_combine_ids(const Ctx& c, const void* y_slots, int y_dtype, c
   if (dtype == MOE_F32) return combine_ids_typed<float, float>(c, y_slots, w, ids, y_shared, T, K, E, H, out);
   if (y_dtype == MOE_F32)
     return combine_ids_typed<float, __nv_bfloat16>(c, y_slots, w, ids, y_shared, T, K, E, H, out);
+  if (y_dtype == kSlotsF16) return combine_ids_typed<__half, __nv_bfloat16>(c, y_slots, w, ids, y_shared, T, K, E, H, out);
   return combine_ids_typed<__nv_bfloat16, __nv_bfloat16>(c, y_slots, w, ids, y_shared, T, K, E, H, out);
 }
 

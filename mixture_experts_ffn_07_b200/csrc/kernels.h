@@ -213,6 +213,9 @@ cudaError_t launch_fp8_front(const Ctx& c, const void* x, int x_dtype, int R, in
                              int32_t* sorted_pairs, int32_t* pair_pos);
 cudaError_t launch_fp8_blocks(const Ctx& c, const void* w, int w_dtype, int G, int N, int K, int fmt, bool pow2,
                               void* q, float* scales);
+// Slot rows as f16 codes [rows, H] with one power of two [rows, ceil(H/128)] (f32, right behind them) for each 128 of a
+// row: a type for launch_combine_ids beside MOE_F32 and MOE_BF16.
+constexpr int kSlotsF16 = -16;
 // out[t] = sum_k w[t,k] y_slots[t*K+k] over the slots with an id in [0, E) (w == nullptr: 1), + y_shared[t].
 cudaError_t launch_combine_ids(const Ctx& c, const void* y_slots, int y_dtype, const float* w, const int32_t* ids,
                                const float* y_shared, int T, int K, int E, int H, void* out, int dtype);
@@ -220,8 +223,8 @@ cudaError_t launch_combine_ids(const Ctx& c, const void* y_slots, int y_dtype, c
 // Grouped product of block-scaled 8-bit floats (fp8_gemm.cu): rows [offsets[g], offsets[g+1]) of A against B0[g]
 // (offsets == nullptr: one group of all rows).
 //  dual = true : h = act(A B0^T) * (A B1^T), coded as e4m3 into out_q [rows, N], out_qs [ceil(N/128), rows]
-//  dual = false: out[dest, n] = scale * (A B0^T)[row, n] in f32 or bf16,
-//                dest = row_map ? row_map[row] : row, scale = row_scale ? row_scale[dest] : 1
+//  dual = false: out[dest, n] = scale * (A B0^T)[row, n] in f32, bf16 or (e4m3 operands and fp8_gemm_many alone, no
+//                row_scale) as kSlotsF16, dest = row_map ? row_map[row] : row, scale = row_scale ? row_scale[dest] : 1
 struct Fp8GemmArgs {
   const void* A;         // codes [rows, K]
   const float* a_scale;  // [ceil(K/128), a_ld]; row r uses column a_scale_map ? a_scale_map[r] / a_scale_div : r
@@ -242,6 +245,8 @@ struct Fp8GemmArgs {
   float* out_qs;
   float* out_f32;
   __nv_bfloat16* out_bf16;
+  __half* out_f16;     // kSlotsF16: the codes, and their powers of two
+  float* out_f16_scale;
   const int32_t* row_map;
   const float* row_scale;
   // The launch before this one on the stream is a gate/up product of this file that began after the weights, scales
@@ -250,6 +255,10 @@ struct Fp8GemmArgs {
   const char* name;
 };
 cudaError_t launch_fp8_gemm(const Ctx& c, const Fp8GemmArgs& a);
+// Whether a launch takes the kernel for groups of many rows.  A bound on the SMs of a device (num_sms above it counts as
+// that many), so that a caller without a device can ask for all of them.
+constexpr int kFp8MaxSms = 256;
+bool fp8_gemm_many(int num_sms, int rows, int N, int G, bool dual);
 // Whether a launch of `rows` rows in G groups takes gathered rows (small batches); others want them in group order.
 bool fp8_gemm_gathers(int rows, int G);
 
