@@ -359,8 +359,8 @@ moe_status moe_q6_k_split(const void* blocks, int64_t rows, int64_t cols, void* 
  *           s_e + b_e in 64 bits (MOE_GROUP_TOP2; of its one in groups of one);
  *           only the topk_groups best (lower index on ties) are eligible
  *   ids     the top_k largest keys in order, the lower expert first on ties
- *   w_k     scale * s_{ids_k}, divided by sum_j s_{ids_j} when renormalize (a
- *           sum of 0 gives weights 0)
+ *   w_k     scale * s_{ids_k}, divided by sum_j s_{ids_j} when renormalize,
+ *           however small the scores are; 0 where all the chosen are masked
  * NaN logits or keys sort like -inf; the ids are distinct and in range whatever
  * the logits hold.  Limits as above (E <= 256, top_k <= 32, n_groups <= 32).
  *

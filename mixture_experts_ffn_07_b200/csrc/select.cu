@@ -130,6 +130,17 @@ __device__ __forceinline__ void scores_of(const float (&l)[kSlots], float m, int
   for (int i = 0; i < kSlots; ++i) s[i] *= inv;
 }
 
+// A chosen expert's score times a factor common to the token's choices, from its logit x and the largest chosen logit,
+// `top` (`mine`: x is one of them; NaN left out): e^(x - top), or with sigmoid, whose score is e^min(x, 0) / (1 + e^-|x|),
+// the same with x - min(top, 0) in the exponent.  The ratios survive where the scores do not: with a bias or groups the
+// chosen softmax scores can all lie below f32's range, 104 under the row's maximum, sigmoid's do for logits below -88.
+__device__ __forceinline__ float shifted_score(float x, bool mine, bool softmax) {
+  const uint32_t k = __reduce_max_sync(kAll, mine && x == x ? Keys<float>::of(x) : 0u);
+  const float top = k ? Keys<float>::value(k) : -INFINITY;
+  if (!mine || x == -INFINITY) return 0.f;
+  return softmax ? expf(x - top) : expf(fminf(x, 0.f) - fminf(top, 0.f)) / (1.f + expf(-fabsf(x)));
+}
+
 // Value that lane `expert % 32` holds for `expert`, in every lane.
 __device__ __forceinline__ float of_expert(const float (&v)[kSlots], int expert) {
   float mine = 0.f;
@@ -468,17 +479,20 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta)
     place = lane;
     x = lane < K ? load_logit(row + e) : 0.f;
   }
-  // the chosen scores again, from their logits; a softmax's own sum only where the weights are not renormalised
-  float sum = 0.f;
-  if (softmax && !c.renorm) {
+  // the chosen scores again, from their logits: over their sum, or a softmax's own
+  float sum = 0.f, v = 0.f;
+  if (c.renorm) {
+    v = shifted_score(x, place < K, softmax);
+    sum = warp_add(v);
+  } else {
+    if (softmax) {
 #pragma unroll
-    for (int i = 0; i < kSlots; ++i)
-      if (!(l[i] == -INFINITY)) sum += expf(l[i] - m);
-    sum = warp_add(sum);
+      for (int i = 0; i < kSlots; ++i)
+        if (!(l[i] == -INFINITY)) sum += expf(l[i] - m);
+      sum = warp_add(sum);
+    }
+    if (place < K) v = x == -INFINITY ? 0.f : softmax ? expf(x - m) : 1.f / (1.f + expf(-x));
   }
-  float v = 0.f;
-  if (place < K) v = x == -INFINITY ? 0.f : softmax ? expf(x - m) : 1.f / (1.f + expf(-x));
-  if (c.renorm) sum = warp_add(v);
   if (place < K) {
     ids[t * K + place] = e;
     if (softmax || c.renorm) v = sum == 0.f ? 0.f : v / sum;

@@ -1,0 +1,77 @@
+"""Selection weights where the chosen scores themselves are too small for f32 and their ratios are not."""
+import math
+
+import pytest
+import torch
+
+import mixture_experts_ffn_07_b200 as moe
+from tests import _fp8ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def _log_scores(l, scoring):
+    """Logarithms of the scores in 64 bits, of softmax without the row's common term."""
+    l = l.double()
+    return l if scoring == "softmax" else l.clamp_max(0) - torch.log1p(torch.exp(-l.abs()))
+
+
+def _ratios(l, ids, scoring):
+    """Chosen scores over their sum, from their logarithms."""
+    s = _log_scores(l, scoring).gather(1, ids)
+    z = torch.exp(s - s.amax(1, keepdim=True))
+    return z / z.sum(1, keepdim=True)
+
+
+def _case(scoring, far, seed, T=40, E=64, K=6):
+    """Logits whose chosen experts (by a bias that outweighs every score) lie `far` below the row's maximum (softmax) or
+    below zero (sigmoid)."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    l = torch.randn((T, E), generator=g, device="cuda") * 2
+    chosen = torch.randperm(E, generator=g, device="cuda")[:K]
+    if scoring == "softmax":
+        l[:, 0] = 8.0
+        chosen = chosen[chosen != 0]
+    l[:, chosen] -= far
+    bias = torch.zeros(E, device="cuda")
+    bias[chosen] = 4.0 + torch.arange(chosen.numel(), device="cuda") / 4
+    return l, bias, chosen.numel(), g
+
+
+def _tol(l, ids):
+    """Relative: an exponent is off by a rounding of its argument, exp by two steps, sum and quotient by a few."""
+    c = l.double().gather(1, ids)
+    return 2 * 2 * ref.U32 * (float((c.amax(1) - c.amin(1)).max()) + 16)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("far", [0.0, 60.0, 86.0, 95.0, 102.0, 104.0, 110.0, 700.0, 5000.0, 1e30])
+def test_weights(scoring, dtype, far):
+    l, bias, K, _ = _case(scoring, far, 3)
+    l = l.to(dtype)
+    T, E = l.shape
+    d = moe.SelectDesc(T=T, E=E, top_k=K, scoring=scoring, scale=2.5)
+    ids, w = torch.empty((T, K), dtype=torch.int32, device="cuda"), torch.full((T, K), math.nan, device="cuda")
+    moe.select(d, l, ids, w, bias=bias)
+    torch.cuda.synchronize()
+    assert moe.last_device_status() == moe.MOE_OK
+    assert set(ids.flatten().tolist()) == set(torch.nonzero(bias).flatten().tolist())
+    want = 2.5 * _ratios(l, ids.long(), scoring)
+    assert torch.all((w.double() - want).abs() <= _tol(l, ids.long()) * want + 1e-37)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_masked_and_single(scoring):
+    """Only masked experts chosen: weights 0.  One eligible expert, however far: weight 1."""
+    T, E, K = 6, 16, 3
+    l = torch.full((T, E), -math.inf, device="cuda")
+    for t, v in enumerate((-1e4, -120.0, 0.0, 90.0)):
+        l[t, 5] = v
+    d = moe.SelectDesc(T=T, E=E, top_k=K, scoring=scoring)
+    ids, w = torch.empty((T, K), dtype=torch.int32, device="cuda"), torch.empty((T, K), device="cuda")
+    moe.select(d, l, ids, w)
+    torch.cuda.synchronize()
+    assert moe.last_device_status() == moe.MOE_OK
+    assert torch.equal(w[:4, 0], torch.ones(4, device="cuda")) and torch.all(ids[:4, 0] == 5)
+    assert torch.all(w[:4, 1:] == 0) and torch.all(w[4:] == 0)
