@@ -387,7 +387,8 @@ moe_status moe_select(const moe_select_desc* d, const void* logits, int64_t stri
 /*
  * Gradient of moe_select's weights (and scores) with the selection held
  * constant.  With n_k = s_k / S, S = sum_k s_k over the chosen experts,
- *   ds_k = scale / S (d_w_k - sum_j d_w_j n_j)   (renormalize; 0 when S is 0)
+ *   ds_k = scale / S (d_w_k - sum_j d_w_j n_j)   (renormalize, however small S is; 0 where all
+ *           the chosen are masked)
  *   ds_k = scale d_w_k                           (otherwise)
  * plus d_scores_e where given (the gradient of a balance loss on the scores);
  *   softmax: d_logits_e = s_e (ds_e - sum_j ds_j s_j);  sigmoid: ds_e s_e (1 - s_e).

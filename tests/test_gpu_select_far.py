@@ -1,4 +1,4 @@
-"""Selection weights where the chosen scores themselves are too small for f32 and their ratios are not."""
+"""Selection weights and their gradient where the chosen scores themselves are too small for f32 and their ratios are not."""
 import math
 
 import pytest
@@ -62,8 +62,43 @@ def test_weights(scoring, dtype, far):
 
 
 @pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("far", [0.0, 86.0, 95.0, 104.0, 700.0, 5000.0])
+@pytest.mark.parametrize("with_scores", [False, True])
+def test_gradient(scoring, dtype, far, with_scores):
+    """d_logits_e = scale n_e (d_w_e - sum_j d_w_j n_j) (1 - s_e with sigmoid), plus the scores' own part."""
+    l, bias, K, g = _case(scoring, far, 4)
+    l = l.to(dtype)
+    T, E = l.shape
+    ids = torch.nonzero(bias).flatten().expand(T, K).contiguous()
+    dw = torch.randn((T, K), generator=g, device="cuda")
+    ds = torch.randn((T, E), generator=g, device="cuda") if with_scores else None
+    d = moe.SelectDesc(T=T, E=E, top_k=K, scoring=scoring, scale=1.5)
+    out = torch.full((T, E), math.nan, dtype=dtype, device="cuda")
+    moe.select_backward(d, l, ids.to(torch.int32), dw, out, d_scores=ds)
+    torch.cuda.synchronize()
+    assert moe.last_device_status() == moe.MOE_OK
+    n, v, s = _ratios(l, ids, scoring), 1.5 * dw.double(), ref.scores(l, scoring)
+    part = n * (v - (v * n).sum(1, keepdim=True))
+    mag = n * (v.abs() + (v.abs() * n).sum(1, keepdim=True))
+    want, size = (torch.zeros_like(s).scatter_add_(1, ids, a) for a in (part, mag))
+    if scoring == "sigmoid":
+        want = want * (1 - s)
+    if with_scores:
+        e = ds.double()
+        dot = (e * s).sum(1, keepdim=True) if scoring == "softmax" else s * e
+        want, size = want + s * (e - dot), size + s * (e.abs() + dot.abs())
+    # factors: a ratio (as for the weights), a score (an exponent up to the row's reach), sums over K and E in f32
+    reach = float((l.double().amax(1) - l.double().amin(1)).clamp_max(110).max())
+    tol = (2 * _tol(l, ids) + (4 * (reach + 16) + 64) * ref.U32) * size
+    if dtype == torch.bfloat16:
+        tol = tol + ref.U16 * want.abs()
+    assert torch.all((out.double() - want).abs() <= tol + 1e-37), float(((out.double() - want).abs() - tol).max())
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
 def test_masked_and_single(scoring):
-    """Only masked experts chosen: weights 0.  One eligible expert, however far: weight 1."""
+    """Only masked experts chosen: weights and gradient 0.  One eligible expert, however far: weight 1."""
     T, E, K = 6, 16, 3
     l = torch.full((T, E), -math.inf, device="cuda")
     for t, v in enumerate((-1e4, -120.0, 0.0, 90.0)):
@@ -71,7 +106,10 @@ def test_masked_and_single(scoring):
     d = moe.SelectDesc(T=T, E=E, top_k=K, scoring=scoring)
     ids, w = torch.empty((T, K), dtype=torch.int32, device="cuda"), torch.empty((T, K), device="cuda")
     moe.select(d, l, ids, w)
+    dl = torch.full((T, E), math.nan, device="cuda")
+    moe.select_backward(d, l, ids, torch.randn((T, K), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda"), dl)
     torch.cuda.synchronize()
     assert moe.last_device_status() == moe.MOE_OK
     assert torch.equal(w[:4, 0], torch.ones(4, device="cuda")) and torch.all(ids[:4, 0] == 5)
     assert torch.all(w[:4, 1:] == 0) and torch.all(w[4:] == 0)
+    assert torch.all(dl == 0)
