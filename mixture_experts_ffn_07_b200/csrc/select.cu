@@ -570,9 +570,9 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta)
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) {
     const int e = lane + 32 * i;
-    if (e < E)
+    if (e < E)  // (1 - s_e with the precision of s_e: the difference of f32 numbers has none left for logits above 16)
       store_grad(d_logits + t * E + e,
-                 softmax ? part[i] + s[i] * (ds[i] - dot) : part[i] * (1.f - s[i]) + ds[i] * s[i] * (1.f - s[i]));
+                 softmax ? part[i] + s[i] * (ds[i] - dot) : (part[i] + ds[i] * s[i]) * (1.f / (1.f + expf(l[i]))));
   }
 }
 

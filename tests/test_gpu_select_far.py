@@ -113,3 +113,37 @@ def test_masked_and_single(scoring):
     assert torch.equal(w[:4, 0], torch.ones(4, device="cuda")) and torch.all(ids[:4, 0] == 5)
     assert torch.all(w[:4, 1:] == 0) and torch.all(w[4:] == 0)
     assert torch.all(dl == 0)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("at", [0.0, 8.0, 14.0, 20.0, 40.0, 80.0])
+def test_gradient_of_saturated_scores(dtype, renorm, at):
+    """Sigmoid scores next to 1: the factor 1 - s = 1 / (1 + e^l) keeps its relative precision."""
+    T, E, K = 50, 48, 4
+    g = torch.Generator(device="cuda").manual_seed(7)
+    l = (torch.randn((T, E), generator=g, device="cuda") + at).to(dtype)
+    dw = torch.randn((T, K), generator=g, device="cuda")
+    ds = torch.randn((T, E), generator=g, device="cuda")
+    d = moe.SelectDesc(T=T, E=E, top_k=K, scoring="sigmoid", renormalize=renorm)
+    ids, w = torch.empty((T, K), dtype=torch.int32, device="cuda"), torch.empty((T, K), device="cuda")
+    moe.select(d, l, ids, w)
+    out = torch.full((T, E), math.nan, dtype=dtype, device="cuda")
+    moe.select_backward(d, l, ids, dw, out, d_scores=ds)
+    torch.cuda.synchronize()
+    assert moe.last_device_status() == moe.MOE_OK
+    ids, x = ids.long(), l.double()
+    s, rest = 1 / (1 + torch.exp(-x)), 1 / (1 + torch.exp(x))
+    v, size = dw.double(), dw.double().abs()
+    if renorm:
+        n = s.gather(1, ids) / s.gather(1, ids).sum(1, keepdim=True)
+        v, size = n * (v - (v * n).sum(1, keepdim=True)), n * (size + (size * n).sum(1, keepdim=True))
+    else:
+        v, size = v * s.gather(1, ids), size * s.gather(1, ids)
+    want = (torch.zeros_like(s).scatter_add_(1, ids, v) + s * ds.double()) * rest
+    size = (torch.zeros_like(s).scatter_add_(1, ids, size) + s * ds.double().abs()) * rest
+    # two scores or ratios, exponents of at most `at` + 6 each (a rounding of the argument, exp by two steps), short sums
+    tol = 2 * (2 * (at + 6 + 16) + K + 8) * ref.U32 * size
+    if dtype == torch.bfloat16:
+        tol = tol + ref.U16 * want.abs()
+    assert torch.all((out.double() - want).abs() <= tol + 1e-37), float(((out.double() - want).abs() / (tol + 1e-37)).max())
