@@ -748,15 +748,24 @@ int resident_clusters(const Ctx& c, int size) {
 // How many CTAs share an item's k-blocks: as many (up to 8, of two k-blocks at least each) as leave every item's
 // cluster resident at once.  Clusters do not fill the GPU (148 SMs hold 74 of two CTAs, but 45 of three, 15 of eight),
 // and a second wave of them costs more than a wider split gains.
+//
+// A split itself costs about 2 us (the cluster's launch, its barriers and sums), so it is taken only where it saves the
+// CTAs that many k-blocks.  Measured, us without / with a split, rows 1 to 64: one product, 16 to 8 k-blocks 9.1 / 10.8
+// (7168 x 2048), 16 to 4 8.4 / 7.5 (2048 x 2048), 28 to 14 12.2 / 12.3, 40 to 20 15.5 / 14.2 (7168 x 5120), 4 to 2 4.8 / 6.6;
+// the dual one of a token's experts, 8 to 4 14.8 / 16.8, 8 to 2 14.8 / 12.9, 16 to 8 18.9 / 16.9.
 template <bool DUAL>
 void set_split(const Ctx& c, Params& p, long long items) {
+  constexpr int kSaved = DUAL ? 6 : 12;
   const int nkb = (p.K + KB - 1) / KB;
-  for (int want = static_cast<int>(std::min<long long>({8LL, c.num_sms / std::max(1LL, items), nkb / 2})); want > 1; --want)
+  for (int want = static_cast<int>(std::min<long long>({8LL, c.num_sms / std::max(1LL, items), nkb / 2})); want > 1; --want) {
+    const int kb_per = (nkb + want - 1) / want;
+    if (nkb - kb_per < kSaved) return;
     if (resident_clusters<DUAL>(c, want) >= items) {
-      p.kb_per = (nkb + want - 1) / want;
-      p.split = (nkb + p.kb_per - 1) / p.kb_per;
+      p.kb_per = kb_per;
+      p.split = (nkb + kb_per - 1) / kb_per;
       return;
     }
+  }
 }
 
 // Items of a launch, no fewer than there can be.
