@@ -768,9 +768,9 @@ void set_split(const Ctx& c, Params& p, long long items) {
   }
 }
 
-// Items of a launch, no fewer than there can be.
+// Items of a launch, no fewer than there can be: c rows of a group are at most (c + NT - 1) / NT tiles.
 long long items_of(int rows, int N, int G) {
-  return static_cast<long long>(rows / NT + std::min(G, rows)) * ((N + WM - 1) / WM);
+  return (rows + static_cast<long long>(std::min(G, rows)) * (NT - 1)) / NT * ((N + WM - 1) / WM);
 }
 
 template <bool DUAL>
@@ -799,7 +799,7 @@ cudaError_t launch_typed(const Ctx& c, const Fp8GemmArgs& a) {
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.split > 1 ? 2 : 1;
-  KernelScope ks(c, a.name ? a.name : "fp8_gemm");
+  KernelScope ks(c, a.name);
   const cudaError_t le = cudaLaunchKernelEx(&cfg, kern, mA, m0, m1, p);
   return le != cudaSuccess ? le : cudaGetLastError();
 }
@@ -811,8 +811,9 @@ double mean_rows(int rows, int G) { return static_cast<double>(rows) / std::max(
 // group 89 / 94, 89 / 90, 32 / 37, 124 / 124 (with 20 rows the other one, by 1 to 5 us); the single one with 6 rows
 // 82 / 85, 79 / 81, 34 / 33, 108 / 110, with 10 rows 88 / 88, 82 / 84, 35 / 33, 126 / 123.  Whatever the rows, it is also
 // faster while its items do not fill the GPU, since they are smaller and share their k-blocks (one product, 16 x 2048 x
-// 7168: 11 / 26, 200 x 2048 x 7168, 112 items: 22 / 33, 500 x 512 x 2048: 12 / 15; but 500 x 2048 x 7168, 256 items:
-// 38 / 33, 96 x 7168 x 2048, 168 items: 16 / 14).
+// 7168: 10.4 / 25.8, 128 x 4096 x 7168, 128 items: 21.3 / 31.0, 512 x 512 x 2048: 10.2 / 12.2; but 512 x 2048 x 7168, 256
+// items: 37.0 / 31.0, 96 x 7168 x 2048, 168 items: 15.3 / 12.5).  The rule knows the mean of a routing alone, which is what
+// the host has: an uneven one's large groups go with the others (a few hundred rows of a mean of 16, in tiles of 32).
 constexpr double kSmallRowsDual = 16.0, kSmallRows = 8.0;
 
 }  // namespace

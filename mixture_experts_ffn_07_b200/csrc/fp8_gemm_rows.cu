@@ -491,12 +491,12 @@ cudaError_t launch_typed(const Ctx& c, const Fp8GemmArgs& a) {
   if (!make_maps(a, TILE_ROWS, &mA, &m0, &m1)) return cudaErrorInvalidValue;
   Params p = make_params(c, a, a.a_fmt, a.b_fmt, TILE_ROWS);
   p.early = a.early;
-  const long long tiles = a.rows / TILE_ROWS + std::min(a.G, a.rows);
+  const long long tiles = (a.rows + static_cast<long long>(std::min(a.G, a.rows)) * (TILE_ROWS - 1)) / TILE_ROWS;
   const long long items = tiles * (DUAL ? p.n_tiles : (p.n_tiles + 1) / 2);
   auto kern = fp8_rows_gemm_kernel<DUAL>;
   const cudaError_t e = allow_dynamic_smem(reinterpret_cast<const void*>(kern), static_cast<int>(SMEM));
   if (e != cudaSuccess) return e;
-  KernelScope ks(c, a.name ? a.name : "fp8_gemm");
+  KernelScope ks(c, a.rows_name);
   return launch_kernel(c, kern, dim3(static_cast<unsigned>(std::min<long long>(c.num_sms, items))), dim3(THREADS), SMEM,
                        mA, m0, m1, p);
 }

@@ -252,7 +252,8 @@ struct Fp8GemmArgs {
   // The launch before this one on the stream is a gate/up product of this file that began after the weights, scales
   // and offsets here were complete (its kernels wait for their predecessors before they let the next launch start).
   bool early;
-  const char* name;
+  const char* name;       // in traces: of the few-row kernel
+  const char* rows_name;  // and of the many-row one
 };
 cudaError_t launch_fp8_gemm(const Ctx& c, const Fp8GemmArgs& a);
 // Whether a launch takes the kernel for groups of many rows.  A bound on the SMs of a device (num_sms above it counts as

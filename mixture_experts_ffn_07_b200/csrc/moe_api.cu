@@ -325,6 +325,7 @@ moe_status fp8_experts(const moe::Ctx& c, const moe_desc& d, const moe_weights& 
   a.out_q = at<void>(ws, L.h);
   a.out_qs = at<float>(ws, L.h_qs);
   a.name = "expert_gate_up_fp8";
+  a.rows_name = "expert_gate_up_fp8_rows";
   MOE_TRY(moe::launch_fp8_gemm(c, a));
   moe::Fp8GemmArgs b{};
   b.A = at<void>(ws, L.h);
@@ -348,6 +349,7 @@ moe_status fp8_experts(const moe::Ctx& c, const moe_desc& d, const moe_weights& 
   b.row_scale = tw;
   b.early = true;
   b.name = "expert_down_fp8";
+  b.rows_name = "expert_down_fp8_rows";
   MOE_TRY(moe::launch_fp8_gemm(c, b));
   return MOE_OK;
 }
@@ -373,6 +375,7 @@ moe_status fp8_shared(const moe::Ctx& c, const moe_desc& d, const moe_weights& w
   a.out_q = at<void>(ws, L.h_s);
   a.out_qs = at<float>(ws, L.hs_qs);
   a.name = "shared_gate_up_fp8";
+  a.rows_name = "shared_gate_up_fp8_rows";
   MOE_TRY(moe::launch_fp8_gemm(c, a));
   moe::Fp8GemmArgs b{};
   b.A = at<void>(ws, L.h_s);
@@ -389,6 +392,7 @@ moe_status fp8_shared(const moe::Ctx& c, const moe_desc& d, const moe_weights& w
   b.row_scale = gate;
   b.early = true;
   b.name = "shared_down_fp8";
+  b.rows_name = "shared_down_fp8_rows";
   MOE_TRY(moe::launch_fp8_gemm(c, b));
   return MOE_OK;
 }
@@ -1124,6 +1128,7 @@ moe_status moe_fp8_gemm(int64_t M, int64_t N, int64_t K, int64_t G, const void* 
   else
     g.out_f32 = static_cast<float*>(out);
   g.name = "fp8_gemm";
+  g.rows_name = "fp8_gemm_rows";
   return from_cuda(moe::launch_fp8_gemm(c, g));
 }
 
