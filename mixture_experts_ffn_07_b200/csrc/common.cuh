@@ -36,6 +36,9 @@ cudaError_t allow_dynamic_smem(const void* kernel, int bytes);
 // previous kernel on the stream is still running: every kernel here calls
 // pdl_wait() before it reads anything an earlier kernel wrote, and
 // pdl_trigger() once all of its CTAs have started.
+// (What an earlier kernel wrote is read with plain loads: the read-only path,
+// __ldg or a const __restrict__ parameter, is for data that nothing writes
+// while the kernel runs, and its CTAs may have started before the writer ended.)
 template <typename... KArgs, typename... Args>
 cudaError_t launch_kernel(const Ctx& c, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                           Args&&... args) {

@@ -405,9 +405,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         float v[AHEAD], t0[AHEAD], t1[AHEAD];
         auto load = [&](int kb, int b) {
           const int k = min(kb, nkb_all - 1);
-          v[b] = __ldg(p.a_scale + k * p.a_ld + at);
-          t0[b] = __ldg(p.s0 + sb + k);
-          t1[b] = DUAL ? __ldg(p.s1 + sb + k) : 0.f;
+          v[b] = p.a_scale[k * p.a_ld + at];
+          t0[b] = p.s0[sb + k];
+          t1[b] = DUAL ? p.s1[sb + k] : 0.f;
         };
 #pragma unroll
         for (int b = 0; b < AHEAD; ++b) load(kb_lo + b, b);

@@ -297,9 +297,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         auto load = [&](int kb, int b) {
           const int k = min(kb, nkb - 1);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) va[b][j] = __ldg(p.a_scale + k * p.a_ld + at[j]);
-          v0[b] = __ldg(t0 + k);
-          v1[b] = __ldg(t1 + k);
+          for (int j = 0; j < 2; ++j) va[b][j] = p.a_scale[k * p.a_ld + at[j]];
+          v0[b] = t0[k];
+          v1[b] = t1[k];
         };
 #pragma unroll
         for (int b = 0; b < AHEAD; ++b) load(b, b);

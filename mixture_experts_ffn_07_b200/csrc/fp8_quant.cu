@@ -30,13 +30,13 @@ struct Raw<__nv_bfloat16> {
 };
 __device__ __forceinline__ Raw<float> load8(const float* p, int left) {
   Raw<float> r;
-  r.a = left > 0 ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0.f, 0.f, 0.f, 0.f);
-  r.b = left > 4 ? __ldg(reinterpret_cast<const float4*>(p) + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+  r.a = left > 0 ? *reinterpret_cast<const float4*>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+  r.b = left > 4 ? *(reinterpret_cast<const float4*>(p) + 1) : make_float4(0.f, 0.f, 0.f, 0.f);
   return r;
 }
 __device__ __forceinline__ Raw<__nv_bfloat16> load8(const __nv_bfloat16* p, int left) {
   Raw<__nv_bfloat16> r;
-  r.a = left > 0 ? __ldg(reinterpret_cast<const uint4*>(p)) : make_uint4(0u, 0u, 0u, 0u);
+  r.a = left > 0 ? *reinterpret_cast<const uint4*>(p) : make_uint4(0u, 0u, 0u, 0u);
   return r;
 }
 __device__ __forceinline__ void values(const Raw<float>& r, float (&v)[8]) {
@@ -91,7 +91,7 @@ struct Coding {  // a thread's values, and the inverse scale of row hl / 4 of it
   float inv;
 };
 template <typename XT>
-__device__ __forceinline__ Coding<XT> load_rows(const XT* __restrict__ x, long long stride, int R, int C, int fmt,
+__device__ __forceinline__ Coding<XT> load_rows(const XT* x, long long stride, int R, int C, int fmt,
                                                 int pow2, long long row_tile, int block_tile, float* sc) {
   const int hw = threadIdx.x >> 4, hl = threadIdx.x & 15;
   const int bl = hw % kTileBlocks;
@@ -122,8 +122,8 @@ __device__ __forceinline__ Coding<XT> load_rows(const XT* __restrict__ x, long l
   return k;
 }
 template <typename XT>
-__device__ __forceinline__ void store_rows(const Coding<XT>& k, int R, int C, int fmt, uint8_t* __restrict__ q,
-                                           float* __restrict__ scales, long long row_tile, int block_tile,
+__device__ __forceinline__ void store_rows(const Coding<XT>& k, int R, int C, int fmt, uint8_t* q,
+                                           float* scales, long long row_tile, int block_tile,
                                            const float* sc, uint8_t* to = nullptr, const int* dest = nullptr,
                                            int copies = 0) {
   const int hw = threadIdx.x >> 4, hl = threadIdx.x & 15;
@@ -154,8 +154,8 @@ __device__ __forceinline__ void store_rows(const Coding<XT>& k, int R, int C, in
 // the coding runs beside it and ends after it (a pass of 100 tokens on 64 experts of 2816 x 704: 88.8 -> 86.8 us).
 template <typename XT>
 __global__ void __launch_bounds__(kRowThreads)
-    fp8_rows_kernel(const XT* __restrict__ x, long long stride, int R, int C, int fmt, int pow2,
-                    uint8_t* __restrict__ q, float* __restrict__ scales, bool early) {
+    fp8_rows_kernel(const XT* x, long long stride, int R, int C, int fmt, int pow2,
+                    uint8_t* q, float* scales, bool early) {
   __shared__ float sc[kTileBlocks * (kTileRows + 1)];
   pdl_trigger();
   if (!early) pdl_wait();
@@ -170,8 +170,8 @@ __global__ void __launch_bounds__(kRowThreads)
 // of a few hundred tokens).  ids, pos: [R, K], the pairs' experts (a copy exists for those in [0, E)) and rows.
 template <typename XT>
 __global__ void __launch_bounds__(kRowThreads)
-    fp8_scatter_kernel(const XT* __restrict__ x, int R, int C, uint8_t* __restrict__ q, float* __restrict__ scales,
-                       uint8_t* __restrict__ to, const int32_t* __restrict__ ids, const int32_t* __restrict__ pos, int K,
+    fp8_scatter_kernel(const XT* x, int R, int C, uint8_t* q, float* scales,
+                       uint8_t* to, const int32_t* ids, const int32_t* pos, int K,
                        int E) {
   __shared__ float sc[kTileBlocks * (kTileRows + 1)];
   __shared__ int dest[kTileRows * kMaxSlots];
@@ -196,10 +196,10 @@ constexpr int kFrontPairs = kRowThreads;
 constexpr int kFrontExperts = 256;
 template <typename XT>
 __global__ void __launch_bounds__(kRowThreads)
-    fp8_front_kernel(const XT* __restrict__ x, int R, int C, uint8_t* __restrict__ q, float* __restrict__ scales,
-                     int row_tiles, const int32_t* __restrict__ ids, int P, int E, int32_t* __restrict__ counts,
-                     int32_t* __restrict__ offsets, int32_t* __restrict__ sorted_pairs,
-                     int32_t* __restrict__ pair_pos, int* status) {
+    fp8_front_kernel(const XT* x, int R, int C, uint8_t* q, float* scales,
+                     int row_tiles, const int32_t* ids, int P, int E, int32_t* counts,
+                     int32_t* offsets, int32_t* sorted_pairs,
+                     int32_t* pair_pos, int* status) {
   __shared__ union {
     float sc[kTileBlocks * (kTileRows + 1)];
     int hist[kRowThreads / 32][kFrontExperts];
@@ -263,8 +263,8 @@ __global__ void __launch_bounds__(kRowThreads)
 // codes, so that they are read once.
 template <typename XT>
 __global__ void __launch_bounds__(kRowThreads)
-    fp8_blocks_kernel(const XT* __restrict__ w, int N, int K, int fmt, int pow2, uint8_t* __restrict__ q,
-                      float* __restrict__ scales) {
+    fp8_blocks_kernel(const XT* w, int N, int K, int fmt, int pow2, uint8_t* q,
+                      float* scales) {
   __shared__ uint32_t part[kRowThreads / 32];
   const int hw = threadIdx.x >> 4, hl = threadIdx.x & 15;
   const int kb = blockIdx.x, nb = blockIdx.y;
@@ -359,8 +359,8 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&v)[N])
 constexpr int kCombineThreads = 256;
 template <typename T, typename OT>
 __global__ void __launch_bounds__(kCombineThreads)
-    combine_ids_kernel(const T* __restrict__ y, const float* __restrict__ w, const int32_t* __restrict__ ids,
-                       const float* __restrict__ y_shared, int K, int E, int H, OT* __restrict__ out) {
+    combine_ids_kernel(const T* y, const float* w, const int32_t* ids,
+                       const float* y_shared, int K, int E, int H, OT* out) {
   constexpr int N = Slots<T>::N;
   constexpr bool kScaled = std::is_same<T, __half>::value;
   constexpr int kAcross = kCombineThreads * N / kFp8Block;  // blocks of 128 outputs
@@ -385,13 +385,13 @@ __global__ void __launch_bounds__(kCombineThreads)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int i = threadIdx.x + j * kCombineThreads, b = blockIdx.y * kAcross + i % kAcross;
-      if (i < K * kAcross && b < blocks) s[j] = __ldg(from + i / kAcross * blocks + b);
+      if (i < K * kAcross && b < blocks) s[j] = from[i / kAcross * blocks + b];
     }
   }
   uint4 r[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    if (j < K) r[j] = __ldg(reinterpret_cast<const uint4*>(row + static_cast<long long>(j) * H));
+    if (j < K) r[j] = *reinterpret_cast<const uint4*>(row + static_cast<long long>(j) * H);
   if (threadIdx.x < K) {
     valid[threadIdx.x] = id >= 0 && id < E;
     weight[threadIdx.x] = my_w;
@@ -411,7 +411,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     if (k0 > 0)
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (k0 + j < K) r[j] = __ldg(reinterpret_cast<const uint4*>(row + static_cast<long long>(k0 + j) * H));
+        if (k0 + j < K) r[j] = *reinterpret_cast<const uint4*>(row + static_cast<long long>(k0 + j) * H);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (k0 + j < K && valid[k0 + j]) {
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kCombineThreads)
     const float* ys = y_shared + t * H + c;
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(ys + i));
+      const float4 v = *reinterpret_cast<const float4*>(ys + i);
       acc[i] += v.x;
       acc[i + 1] += v.y;
       acc[i + 2] += v.z;

@@ -450,8 +450,8 @@ __device__ __forceinline__ bool choose32(const LT* row, const float (&l)[kSlots]
 
 template <typename LT>
 __global__ void __launch_bounds__(32 * kWarpsPerCta)
-    select_kernel(const LT* __restrict__ logits, long long stride, const float* __restrict__ bias, SelectCfg c,
-                  int32_t* __restrict__ ids, float* __restrict__ w, float* __restrict__ scores) {
+    select_kernel(const LT* logits, long long stride, const float* bias, SelectCfg c,
+                  int32_t* ids, float* w, float* scores) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   pdl_wait();
@@ -504,9 +504,9 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta)
 
 template <typename LT>
 __global__ void __launch_bounds__(32 * kWarpsPerCta)
-    select_backward_kernel(const LT* __restrict__ logits, long long stride, const int32_t* __restrict__ ids,
-                           const float* __restrict__ d_w, const float* __restrict__ d_scores, SelectCfg c,
-                           LT* __restrict__ d_logits, int* status) {
+    select_backward_kernel(const LT* logits, long long stride, const int32_t* ids,
+                           const float* d_w, const float* d_scores, SelectCfg c,
+                           LT* d_logits, int* status) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   pdl_wait();
