@@ -29,14 +29,14 @@ constexpr int kColsInFlight = 4;
 
 __device__ __forceinline__ float4 ld_once4(const float4* p) {
   float4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "l"(p));
   return v;
 }
 __device__ __forceinline__ float ld_once(const float* p) {
   float v;
-  asm volatile("ld.global.nc.L1::no_allocate.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.f32 %0, [%1];" : "=f"(v) : "l"(p));
   return v;
 }
 
@@ -49,8 +49,8 @@ __device__ __forceinline__ float4 ld_col(const float* row, long long j) {
 // d_out rows are read by each of the token's K slots: keep them cacheable.
 template <int VEC>
 __device__ __forceinline__ float4 ld_col_l2(const float* row, long long j) {
-  if constexpr (VEC == 4) return __ldg(reinterpret_cast<const float4*>(row) + j);
-  return make_float4(__ldg(row + j), 0.f, 0.f, 0.f);
+  if constexpr (VEC == 4) return reinterpret_cast<const float4*>(row)[j];
+  return make_float4(row[j], 0.f, 0.f, 0.f);
 }
 template <int VEC>
 __device__ __forceinline__ void st_col(float* row, long long j, float4 v) {
@@ -69,9 +69,9 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float acc) {
 __device__ __forceinline__ float4 scale4(float s, float4 v) { return make_float4(s * v.x, s * v.y, s * v.z, s * v.w); }
 
 template <int VEC>
-__global__ void __launch_bounds__(kCombineThreads) combine_backward_kernel(const float* __restrict__ y,
-                                                                           const float* __restrict__ w,
-                                                                           const float* __restrict__ d_out, long long P,
+__global__ void __launch_bounds__(kCombineThreads) combine_backward_kernel(const float* y,
+                                                                           const float* w,
+                                                                           const float* d_out, long long P,
                                                                            int K, long long H, float* __restrict__ d_y,
                                                                            float* __restrict__ d_w) {
   pdl_trigger();
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_backward_kernel(const
   const float* yrow = y + p * H;
   const float* drow = d_out + (p / K) * H;
   float* orow = d_y + p * H;
-  const float wk = __ldg(w + p);
+  const float wk = w[p];
   float acc = 0.f;
   for (long long j0 = lane; j0 < ncol; j0 += 32 * kColsInFlight) {
     float4 yv[kColsInFlight], dv[kColsInFlight];
@@ -144,8 +144,8 @@ __device__ __forceinline__ void act_up_cols(int act, float4 g, float4 u, float4 
 // Elementwise over the P x I/VEC column groups; each thread takes two groups
 // (its index and the one a grid further on) per iteration, loads first.
 template <int VEC>
-__global__ void __launch_bounds__(kBwdThreads) act_up_backward_kernel(const float* __restrict__ gate_up,
-                                                                      const float* __restrict__ d_h, long long P,
+__global__ void __launch_bounds__(kBwdThreads) act_up_backward_kernel(const float* gate_up,
+                                                                      const float* d_h, long long P,
                                                                       long long I, int act,
                                                                       float* __restrict__ d_gate_up) {
   pdl_trigger();

@@ -26,11 +26,11 @@ constexpr int kMaxE = 256;
 constexpr int kBatch = 8;  // 32-pair rounds whose ids are loaded together
 constexpr int kCluster = 8;
 
-__global__ void __launch_bounds__(kWarps * 32) permute_kernel(const int32_t* __restrict__ ids, int P, int E,
-                                                               int32_t* __restrict__ counts,
-                                                               int32_t* __restrict__ offsets,
-                                                               int32_t* __restrict__ sorted_pairs,
-                                                               int32_t* __restrict__ pair_pos, int* status) {
+__global__ void __launch_bounds__(kWarps * 32) permute_kernel(const int32_t* ids, int P, int E,
+                                                               int32_t* counts,
+                                                               int32_t* offsets,
+                                                               int32_t* sorted_pairs,
+                                                               int32_t* pair_pos, int* status) {
   __shared__ int hist[kWarps][kMaxE];  // per (warp segment, expert): count, later running base
   __shared__ int tot[kMaxE];
   __shared__ int excl[kMaxE + 1];
@@ -142,11 +142,11 @@ __global__ void __launch_bounds__(kWarps * 32) permute_kernel(const int32_t* __r
 constexpr int kMaxPerThread = 8;
 
 template <int kPerThread>
-__global__ void __launch_bounds__(kWarps * 32) permute_cluster_kernel(const int32_t* __restrict__ ids, int P, int E,
-                                                                       int32_t* __restrict__ counts,
-                                                                       int32_t* __restrict__ offsets,
-                                                                       int32_t* __restrict__ sorted_pairs,
-                                                                       int32_t* __restrict__ pair_pos, int* status) {
+__global__ void __launch_bounds__(kWarps * 32) permute_cluster_kernel(const int32_t* ids, int P, int E,
+                                                                       int32_t* counts,
+                                                                       int32_t* offsets,
+                                                                       int32_t* sorted_pairs,
+                                                                       int32_t* pair_pos, int* status) {
   __shared__ int hist[kWarps][kMaxE];
   __shared__ int tot[kMaxE];   // this CTA's pairs per expert (read by the other CTAs)
   __shared__ int excl[kMaxE + 1];
@@ -254,10 +254,10 @@ __global__ void __launch_bounds__(kWarps * 32) permute_cluster_kernel(const int3
 }
 
 // One warp per destination row; each lane moves 16-byte chunks, four in flight.
-__global__ void __launch_bounds__(256) gather_rows_kernel(const uint4* __restrict__ x,
-                                                          const int32_t* __restrict__ sorted_pairs,
-                                                          const int32_t* __restrict__ offsets, int E, int K, int P,
-                                                          int chunks_per_row, uint4* __restrict__ out) {
+__global__ void __launch_bounds__(256) gather_rows_kernel(const uint4* x,
+                                                          const int32_t* sorted_pairs,
+                                                          const int32_t* offsets, int E, int K, int P,
+                                                          int chunks_per_row, uint4* out) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();
   pdl_wait();
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(256) gather_rows_kernel(const uint4* __restric
       uint4 v[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        if (c0 + 32 * u < chunks_per_row) v[u] = __ldg(src + c0 + 32 * u);
+        if (c0 + 32 * u < chunks_per_row) v[u] = src[c0 + 32 * u];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         if (c0 + 32 * u < chunks_per_row) dst[c0 + 32 * u] = v[u];

@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) front_kernel(const FrontArgs a) {
       uint4 v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (o + 32 * j < n16) v[j] = __ldg(s + o + 32 * j);
+        if (o + 32 * j < n16) v[j] = s[o + 32 * j];
       for (int q = q0; q < q1; ++q) {
         uint4* d = dst + static_cast<size_t>(pos_in_smem ? s_pos[q - p0] : a.pair_pos[q]) * n16;
 #pragma unroll

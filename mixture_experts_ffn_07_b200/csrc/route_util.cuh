@@ -34,6 +34,14 @@ __device__ __forceinline__ void raw_load(const float* p, Raw8<float>& r) {
 __device__ __forceinline__ void raw_load(const __nv_bfloat16* p, Raw8<__nv_bfloat16>& r) {
   r.a = __ldg(reinterpret_cast<const uint4*>(p));
 }
+// The same of what an earlier launch may have written (see launch_kernel).
+__device__ __forceinline__ void raw_load_written(const float* p, Raw8<float>& r) {
+  r.a = reinterpret_cast<const uint4*>(p)[0];
+  r.b = reinterpret_cast<const uint4*>(p)[1];
+}
+__device__ __forceinline__ void raw_load_written(const __nv_bfloat16* p, Raw8<__nv_bfloat16>& r) {
+  r.a = *reinterpret_cast<const uint4*>(p);
+}
 __device__ __forceinline__ void raw_decode(const Raw8<float>& r, float (&v)[8]) {
   v[0] = __uint_as_float(r.a.x); v[1] = __uint_as_float(r.a.y); v[2] = __uint_as_float(r.a.z);
   v[3] = __uint_as_float(r.a.w); v[4] = __uint_as_float(r.b.x); v[5] = __uint_as_float(r.b.y);
@@ -195,7 +203,7 @@ __device__ __forceinline__ void warp_select(const float (&v)[8], float m, const 
 
 // warp_select on the E raw logits of `row` (global or shared memory) plus the
 // bias; the biased logits go to logits_out (a different array than row).
-__device__ __forceinline__ void warp_topk(const float* __restrict__ row, const float* __restrict__ bias,
+__device__ __forceinline__ void warp_topk(const float* row, const float* __restrict__ bias,
                                           const RouteCfg& rc, float* __restrict__ logits_out,
                                           int32_t* __restrict__ ids, float* __restrict__ wout) {
   const int lane = threadIdx.x & 31;
@@ -222,7 +230,7 @@ __device__ __forceinline__ void warp_topk(const float* __restrict__ row, const f
 // expert e of token t (T*E floats each, `stride` apart), added in part order.
 // A lane takes EP of its experts per round, all their parts requested together.
 template <int EP>
-__device__ __forceinline__ void sum_parts(const float* __restrict__ parts, int nparts, size_t stride, int E, int t,
+__device__ __forceinline__ void sum_parts(const float* parts, int nparts, size_t stride, int E, int t,
                                           float* srow) {
   constexpr int KP = 16 / EP;
   const int lane = threadIdx.x & 31;
@@ -284,7 +292,7 @@ __device__ __forceinline__ void topk_token(const float* parts, int nparts, size_
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
         if (base + 256 * u < H) {
-          raw_load(xr + base + 256 * u, xv[u]);
+          raw_load_written(xr + base + 256 * u, xv[u]);
           raw_load(w_s + base + 256 * u, wv[u]);
         }
 #pragma unroll

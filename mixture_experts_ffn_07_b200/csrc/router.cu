@@ -78,7 +78,7 @@ static_assert(kStageBytes / (kClusterTok * 4) == kRouterChunk, "router chunking 
 
 template <typename XT, typename WT>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(256)
-    router_cluster_kernel(const XT* __restrict__ x, const WT* __restrict__ W, const WT* __restrict__ w_s,
+    router_cluster_kernel(const XT* x, const WT* __restrict__ W, const WT* __restrict__ w_s,
                           const float* __restrict__ bias, int T, int H, const RouteCfg rc,
                           float* __restrict__ logits, int32_t* __restrict__ ids, float* __restrict__ wout,
                           float* __restrict__ shared_gate) {
@@ -108,7 +108,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(256)
     for (int i = threadIdx.x; i < nt * opr; i += blockDim.x) {
       const int c = i / opr, q = i - c * opr;
       Raw8<XT> r;
-      raw_load(x + static_cast<size_t>(t0 + c) * H + h0 + 8 * q, r);
+      raw_load_written(x + static_cast<size_t>(t0 + c) * H + h0 + 8 * q, r);
       float v[8];
       raw_decode(r, v);
       float4* dst = reinterpret_cast<float4*>(xs + c * kHc + 8 * q);
@@ -148,11 +148,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(256)
 // result is deterministic) into `logits` before selection.  With w_s the warp
 // also computes the shared gate sigmoid(w_s . x[t]).
 template <typename XT, typename WT>
-__global__ void __launch_bounds__(256) router_topk_kernel(const float* __restrict__ parts, int nparts,
+__global__ void __launch_bounds__(256) router_topk_kernel(const float* parts, int nparts,
                                                           size_t part_stride, float* __restrict__ logits,
                                                           const float* __restrict__ bias, int T,
                                                           const RouteCfg rc, int32_t* __restrict__ ids,
-                                                          float* __restrict__ wout, const XT* __restrict__ x,
+                                                          float* __restrict__ wout, const XT* x,
                                                           const WT* __restrict__ w_s, int H,
                                                           float* __restrict__ shared_gate) {
   __shared__ float s_row[8][256];  // one logit row per warp

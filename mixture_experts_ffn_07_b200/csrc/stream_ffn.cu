@@ -9,8 +9,8 @@ namespace {
 // One thread per (token, float4 column) item, grid-stride; IT is the index
 // type (32-bit whenever the item count allows, which keeps the row division cheap).
 template <typename OT, typename IT>
-__global__ void __launch_bounds__(256) combine_kernel(const float4* __restrict__ y_slots,
-                                                      const float4* __restrict__ y_shared, int T, int K, int H4,
+__global__ void __launch_bounds__(256) combine_kernel(const float4* y_slots,
+                                                      const float4* y_shared, int T, int K, int H4,
                                                       OT* __restrict__ out) {
   pdl_trigger();
   pdl_wait();
@@ -21,11 +21,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const float4* __restrict__
     const IT c = idx - t * H4;
     const float4* ys = y_slots + (t * K) * H4 + c;
     float4 v[8];
-    float4 acc = __ldg(ys);
+    float4 acc = *ys;
     for (int k0 = 1; k0 < K; k0 += 8) {  // up to eight slot rows in flight, added in k order
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (k0 + j < K) v[j] = __ldg(ys + static_cast<IT>(k0 + j) * H4);
+        if (k0 + j < K) v[j] = ys[static_cast<IT>(k0 + j) * H4];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (k0 + j < K) {
@@ -36,7 +36,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const float4* __restrict__
         }
     }
     if (y_shared) {
-      const float4 w = __ldg(y_shared + t * H4 + c);
+      const float4 w = y_shared[t * H4 + c];
       acc.x += w.x;
       acc.y += w.y;
       acc.z += w.z;
@@ -84,8 +84,8 @@ __device__ __forceinline__ float4 bf16x4_f4(uint2 v) {
 }
 
 template <typename IT>
-__global__ void __launch_bounds__(256) combine_w_kernel(const uint2* __restrict__ ys, const float* __restrict__ w,
-                                                        const float4* __restrict__ y_shared, int T, int K, int H4,
+__global__ void __launch_bounds__(256) combine_w_kernel(const uint2* ys, const float* w,
+                                                        const float4* y_shared, int T, int K, int H4,
                                                         __nv_bfloat16* __restrict__ out) {
   pdl_trigger();
   pdl_wait();
@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(256) combine_w_kernel(const uint2* __restrict_
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (k0 + j < K) {
-          v[j] = __ldg(base + static_cast<IT>(k0 + j) * H4);
-          wk[j] = __ldg(wt + k0 + j);
+          v[j] = base[static_cast<IT>(k0 + j) * H4];
+          wk[j] = wt[k0 + j];
         }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(256) combine_w_kernel(const uint2* __restrict_
         }
     }
     if (y_shared) {
-      const float4 s4 = __ldg(y_shared + t * H4 + c);
+      const float4 s4 = y_shared[t * H4 + c];
       acc.x += s4.x;
       acc.y += s4.y;
       acc.z += s4.z;

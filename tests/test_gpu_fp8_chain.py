@@ -63,3 +63,51 @@ def test_training_step_back_to_back(T, H, E, I, K):
     for i, r in enumerate(got):
         for k, (a, b) in enumerate(zip(r, want[i % n])):
             assert torch.equal(a, b), (i, k)
+
+
+@pytest.mark.parametrize("T,dtype,w_dtype", [(5, "bf16", "bf16"), (100, "bf16", "bf16"), (400, "bf16", "bf16"), (3, "f32", "f32"),
+                                             (90, "f32", "f32"), (90, "bf16", "fp8"), (900, "bf16", "fp8")])
+def test_layers_back_to_back(T, dtype, w_dtype):
+    """A layer on the layer before it, and the gradient of its combine: each call reads what the one before it writes."""
+    H, E, I, K = 256, 32, 96, 4
+    g = _gen(T)
+    at = torch.bfloat16 if dtype == "bf16" else torch.float32
+    d = moe.Desc(T=T, H=H, E=E, I=I, top_k=K, act_dtype=dtype, w_dtype=w_dtype, router_dtype=dtype)
+    layers = []
+    for i in range(2):
+        router = (torch.randn((E, H), generator=g, device="cuda") / 16).to(at)
+        if w_dtype == "fp8":
+            layers.append(moe.Weights(router=router, **_fp8_weights(E, H, I, 0, T + i)))
+        else:
+            layers.append(moe.Weights(router=router, **{n: (torch.randn(s, generator=g, device="cuda") / 8).to(at) for n, s in
+                                                       dict(gate=(E, I, H), up=(E, I, H), down=(E, H, I)).items()}))
+    n = 3
+    xs = (torch.randn((n, T, H), generator=g, device="cuda")).to(at)
+    a, b, ws = torch.empty_like(xs[0]), torch.empty_like(xs[0]), torch.empty(moe.workspace_bytes(d), dtype=torch.uint8, device="cuda")
+    logits, ids, tw = torch.empty((T, E), device="cuda"), torch.empty((T, K), dtype=torch.int32, device="cuda"), torch.empty((T, K), device="cuda")
+    counts, offs = torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty(E + 1, dtype=torch.int32, device="cuda")
+    sp, pp = (torch.empty(T * K, dtype=torch.int32, device="cuda") for _ in range(2))
+    y, dy, dw = torch.empty((T * K, H), device="cuda"), torch.empty((T, K, H), device="cuda"), torch.empty((T, K), device="cuda")
+    z = torch.empty_like(a)
+
+    def step(i, sync):
+        def call(f, *args):
+            f(*args)
+            if sync:
+                torch.cuda.synchronize()
+
+        call(moe.layer, d, xs[i], layers[0], a, ws)
+        call(moe.layer, d, a, layers[1], b, ws)
+        call(moe.route, d, b, layers[0], logits, ids, tw, None, ws)
+        call(moe.permute, d, ids, counts, offs, sp, pp)
+        call(moe.expert_ffn, d, b, layers[0], offs, sp, tw, y, ws)
+        call(moe.combine, d, y, b, layers[0], None, z, ws)
+        call(moe.combine_backward, y.view(T, K, H), tw, y.view(T, K, H)[:, 0].contiguous(), dy, dw)
+        return [v.clone() for v in (a, b, logits, ids, tw, offs, sp, y, z, dy, dw)]
+
+    want = [step(i, True) for i in range(n)]
+    got = [step(i % n, False) for i in range(8 * n)]
+    _ok()
+    for i, r in enumerate(got):
+        for k, (p, q) in enumerate(zip(r, want[i % n])):
+            assert torch.equal(p, q), (i, k)
