@@ -33,12 +33,23 @@ struct Ctx {
 cudaError_t allow_dynamic_smem(const void* kernel, int bytes);
 
 // Launch `kernel` on ctx.stream.  With ctx.pdl the launch may start while the
-// previous kernel on the stream is still running: every kernel here calls
-// pdl_wait() before it reads anything an earlier kernel wrote, and
-// pdl_trigger() once all of its CTAs have started.
-// (What an earlier kernel wrote is read with plain loads: the read-only path,
+// previous kernel on the stream is still running, as soon as every CTA of that
+// one has called pdl_trigger() or ended.  Two kinds of kernels:
+//  * Ordinary ones call pdl_wait() before they read or write anything that an
+//    earlier kernel uses; pdl_trigger() may come before it.
+//  * Early ones work in front of their pdl_wait() on what was complete before
+//    their PREDECESSOR's wait ended: fp8_scatter_kernel and fp8_rows_kernel
+//    (early) on x behind a permutation, the down products (early) on weights
+//    and offsets behind their gate/up product, the tail launch of a bf16 GEMM
+//    behind its CTA-pair launch.  So those predecessors -- the permutation
+//    kernels, fp8_gemm_kernel, fp8_rows_gemm_kernel, the CTA-pair GEMM -- call
+//    pdl_trigger() AFTER pdl_wait() in every CTA, and nothing may be launched
+//    between the two.  An early kernel calls pdl_wait() before it ends, so that
+//    whoever waits for it has waited for its predecessor too.
+// What an earlier kernel wrote is read with plain loads: the read-only path,
 // __ldg or a const __restrict__ parameter, is for data that nothing writes
-// while the kernel runs, and its CTAs may have started before the writer ended.)
+// while the kernel runs, its CTAs may have started before the writer ended, and
+// the compiler may move such a load in front of the wait.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_kernel(const Ctx& c, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                           Args&&... args) {
