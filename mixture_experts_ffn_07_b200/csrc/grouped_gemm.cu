@@ -111,14 +111,19 @@ struct KParams {
                        // (the CTA-pair kernel's full 256-row tiles); 0: all rows
   const int32_t* gather_rows;  // A row r = row gather_rows[r] / gather_div of the map's tensor (nullptr: row r)
   int gather_div;
+  int gather_src;              // rows of that tensor
 };
 
-// Token rows of A rows [a_row + 4 lane, a_row + 4 lane + 4) for a gathered A operand (rows past the last
-// logical row read the last one; the epilogue never writes them).
+// Token rows of A rows [a_row + 4 lane, a_row + 4 lane + 4) for a gathered A operand.  Rows past the group's
+// read what stands there (the epilogue never writes them): rows past the last logical one the last, and pairs
+// of no expert, which leave the end of gather_rows unwritten, some row inside the tensor.
 __device__ __forceinline__ void gather_tokens(const KParams& p, int a_row, int (&tr)[4]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) tr[j] = p.gather_rows[min(a_row + 4 * lane + j, p.rows_single - 1)] / p.gather_div;
+  for (int j = 0; j < 4; ++j) {
+    const int t = p.gather_rows[min(a_row + 4 * lane + j, p.rows_single - 1)] / p.gather_div;
+    tr[j] = min(max(t, 0), p.gather_src - 1);
+  }
 }
 
 // Wait ignoring the abort flag (used to drain in-flight work before exit).
@@ -826,6 +831,7 @@ KParams make_params(const Ctx& c, const GemmArgs& a, int col_step, int head_mult
   p.head_mult = head_mult;
   p.gather_rows = a.gather_rows;
   p.gather_div = a.gather_div > 0 ? a.gather_div : 1;
+  p.gather_src = a.rows_src;
   return p;
 }
 
