@@ -198,7 +198,8 @@ Layout layout_of(const moe_desc& d) {
   L.sorted_pairs = take(P * 4);
   L.pair_pos = take(P * 4);
   L.y_slots = take(f8 ? fp8_slot_bytes(d) : P * H * 4);
-  L.x_perm = f8 ? take(P * H) : tc && !g_tma_gather.load() ? take(P * H * 2) : 0;
+  // (small batches of 8-bit-float experts gather their rows)
+  L.x_perm = f8 ? (moe::fp8_gemm_gathers(d.T * d.top_k, d.E) ? 0 : take(P * H)) : tc && !g_tma_gather.load() ? take(P * H * 2) : 0;
   L.h = take(P * I * (f8 ? 1 : tc ? 2 : 4));
   L.h_s = Is ? take(T * Is * (f8 ? 1 : tc ? 2 : 4)) : 0;
   L.y_s = Is ? take(T * H * 4) : 0;
