@@ -15,8 +15,9 @@
 // many steps.  The choice itself: the K-th largest of the 32 lanes' largest keys bounds the K-th largest of all from
 // below; the few keys not under it (20 or so of 256) move to a lane each, which counts the keys before its own.  That
 // is two thirds fewer instructions than a sort in every lane and K rounds of a maximum over the warp, which took 24 us
-// for 8192 tokens of 256 experts in 8 groups; now 12 us, of 1000 instructions a token, still bound by issue and the integer
-// units, not by the 8.9 MB read and written.
+// for 8192 tokens of 256 experts in 8 groups; now 12 us, of 1030 instructions a token, for the 8.9 MB read and written:
+// bound by dependent instructions at the five warps a scheduler that 80 registers allow (one issued every 8.4 cycles of
+// a warp), no pipe being full.
 //
 // Backward with the selection held constant: with n_k = s_k / S, S = sum_k s_k,
 //   ds_k = scale / S (dw_k - sum_j dw_j n_j)  (renormalised)  or  scale dw_k,  plus d_scores;
