@@ -22,8 +22,8 @@
 // Backward with the selection held constant: with n_k = s_k / S, S = sum_k s_k,
 //   ds_k = scale / S (dw_k - sum_j dw_j n_j)  (renormalised)  or  scale dw_k,  plus d_scores;
 //   softmax: dl_e = s_e (ds_e - sum_j ds_j s_j);  sigmoid: dl_e = ds_e s_e (1 - s_e).
-// Renormalised, the products s_k ds_k = scale n_k (dw_k - sum_j dw_j n_j) are formed without s_k and S, which can be too
-// small for f32 where n_k is not; their sum over k is 0.
+// Renormalised, with a chosen score below 2^-60, the products s_k ds_k = scale n_k (dw_k - sum_j dw_j n_j) are formed
+// without s_k and S, which can be too small for f32 where n_k is not; their sum over k is 0.
 #include "kernels.h"
 
 namespace moe {
@@ -534,20 +534,34 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta)
   }
   const bool softmax = c.scoring == MOE_GATING_SOFTMAX;
   scores_of<float, false>(l, softmax ? row_max(l) : 0.f, c.scoring, s);
-  if (c.renorm) {  // my_dw becomes the slot's n_k (dw_k - sum_j dw_j n_j), the product s_k ds_k
-    float my_l = 0.f;
+  bool far = false;  // of the chosen scores one is too small for what follows in f32 (or masked)
+  if (c.renorm) {
+    float my_s = 0.f;
     for (int k = 0; k < K; ++k) {
       const int id = __shfl_sync(kAll, my_id, k);
-      const float v = of_expert(l, max(id, 0));
-      if (lane == k) my_l = v;
+      const float v = of_expert(s, max(id, 0));
+      if (lane == k && id >= 0) my_s = v;
     }
-    float n = shifted_score(my_l, my_id >= 0, softmax);
-    const float sum = warp_add(n);
-    n = sum == 0.f ? 0.f : n / sum;
-    const float mean = warp_add(my_id >= 0 ? my_dw * n : 0.f);
-    my_dw = n * (my_dw - mean);
+    far = __any_sync(kAll, my_id >= 0 && my_s < 0x1p-60f);
+    if (!far) {
+      const float sum = warp_add(my_s);
+      const float mean = warp_add(my_id >= 0 ? my_dw * my_s : 0.f);
+      my_dw = sum == 0.f ? 0.f : (my_dw - mean / sum) / sum;
+    } else {  // my_dw becomes the slot's n_k (dw_k - sum_j dw_j n_j), the product s_k ds_k
+      float my_l = 0.f;
+      for (int k = 0; k < K; ++k) {
+        const int id = __shfl_sync(kAll, my_id, k);
+        const float v = of_expert(l, max(id, 0));
+        if (lane == k) my_l = v;
+      }
+      float n = shifted_score(my_l, my_id >= 0, softmax);
+      const float sum = warp_add(n);
+      n = sum == 0.f ? 0.f : n / sum;
+      const float mean = warp_add(my_id >= 0 ? my_dw * n : 0.f);
+      my_dw = n * (my_dw - mean);
+    }
   }
-  float part[kSlots];  // renorm: the weights' part of s_e ds_e
+  float part[kSlots];  // far: the weights' part of s_e ds_e
 #pragma unroll
   for (int i = 0; i < kSlots; ++i) part[i] = 0.f;
   for (int k = 0; k < K; ++k) {  // in slot order, so that an expert named twice sums the same way every time
@@ -556,13 +570,13 @@ __global__ void __launch_bounds__(32 * kWarpsPerCta)
 #pragma unroll
     for (int i = 0; i < kSlots; ++i)
       if (lane + 32 * i == id) {
-        if (c.renorm)
+        if (far)
           part[i] += d;
         else
           ds[i] += d;
       }
   }
-  float dot = 0.f;  // (the weights' part of it is 0 when they are renormalised)
+  float dot = 0.f;  // (far: the weights' part of it is 0)
   if (softmax) {
 #pragma unroll
     for (int i = 0; i < kSlots; ++i) dot += ds[i] * s[i];

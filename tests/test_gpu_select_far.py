@@ -88,6 +88,8 @@ def test_gradient(scoring, dtype, far, with_scores):
         e = ds.double()
         dot = (e * s).sum(1, keepdim=True) if scoring == "softmax" else s * e
         want, size = want + s * (e - dot), size + s * (e.abs() + dot.abs())
+    if scoring == "softmax":  # sum_j s_j ds_j over the weights' part is 0, and in f32 a rounding of its terms
+        size = size + s * mag.sum(1, keepdim=True)
     # factors: a ratio (as for the weights), a score (an exponent up to the row's reach), sums over K and E in f32
     reach = float((l.double().amax(1) - l.double().amin(1)).clamp_max(110).max())
     tol = (2 * _tol(l, ids) + (4 * (reach + 16) + 64) * ref.U32) * size
